@@ -6,6 +6,7 @@ shared library is missing the import fails loudly; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -55,12 +56,27 @@ EXPORTED = (
     "qlora_mlp_workspace_size",
     "qlora_mlp_forward",
     "qlora_mlp_backward",
+    "qlora_act8_sizes",
+    "qlora_act8_quantize",
+    "qlora_act8_dequantize",
+    "qlora_swiglu_forward_act8",
+    "qlora_swiglu_backward_act8",
+    "qlora_linear_backward_act8",
+    "qlora_mlp_forward_act8",
+    "qlora_mlp_backward_act8",
+    "qlora_rmsnorm_forward",
+    "qlora_rmsnorm_workspace_size",
+    "qlora_rmsnorm_backward",
 )
 
 QLORA_SCALES_FP32 = 0
 QLORA_SCALES_E4M3 = 1
 QLORA_SCALES_E5M2 = 2
 QLORA_SCALES_U8 = 3
+
+QLORA_ACT8_INT8 = 0
+QLORA_ACT8_E4M3 = 1
+ACT8_BLOCK = 64
 
 
 class QloraError(RuntimeError):
@@ -135,6 +151,16 @@ class _MlpGrads(ctypes.Structure):
                 ("dA_gate", "dB_gate", "dA_up", "dB_up", "dA_down", "dB_down")]
 
 
+class _Act8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("code", ctypes.c_int32)]
+
+
+class _MlpSaved8(ctypes.Structure):
+    _fields_ = [("g", _Act8), ("u", _Act8), ("T_gate", ctypes.c_void_p),
+                ("T_up", ctypes.c_void_p), ("T_down", ctypes.c_void_p)]
+
+
 class _AdamConfig(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float),
@@ -183,6 +209,20 @@ def lib() -> ctypes.CDLL:
         bwd = [vp, vp, i64, tp, vp, vp, i32, f32, vp, vp, vp, vp, i32, vp, ctypes.c_size_t, vp]
         L.qlora_linear_forward.argtypes = fwd
         L.qlora_linear_backward.argtypes = bwd
+        a8, s8 = ctypes.POINTER(_Act8), ctypes.POINTER(_MlpSaved8)
+        gp, cz = ctypes.POINTER(_MlpGrads), ctypes.c_size_t
+        L.qlora_act8_sizes.argtypes = [i64, i64, sz, sz]
+        L.qlora_act8_quantize.argtypes = [vp, a8, vp]
+        L.qlora_act8_dequantize.argtypes = [a8, vp, vp]
+        L.qlora_swiglu_forward_act8.argtypes = [vp, vp, vp, a8, a8, vp]
+        L.qlora_swiglu_backward_act8.argtypes = [vp, a8, a8, vp, vp, vp, vp]
+        L.qlora_linear_backward_act8.argtypes = [vp, a8, tp, vp, vp, i32, f32, vp, vp, vp, vp, i32,
+                                                 vp, cz, vp]
+        L.qlora_mlp_forward_act8.argtypes = [vp, mp, f32, vp, s8, vp, cz, vp]
+        L.qlora_mlp_backward_act8.argtypes = [vp, a8, mp, f32, s8, vp, gp, i32, vp, cz, vp]
+        L.qlora_rmsnorm_forward.argtypes = [vp, vp, vp, i64, i64, f32, vp, vp, a8, vp]
+        L.qlora_rmsnorm_workspace_size.argtypes = [i64, i64, sz]
+        L.qlora_rmsnorm_backward.argtypes = [vp, vp, vp, vp, i64, i64, f32, vp, vp, i32, vp, cz, vp]
         L.qlora_linear_forward_ex.argtypes = fwd + [ctypes.c_void_p]
         L.qlora_linear_backward_ex.argtypes = bwd + [ctypes.c_void_p]
         for name in EXPORTED[1:]:
@@ -608,3 +648,343 @@ def qlora_mlp_backward(dY: torch.Tensor, X: torch.Tensor, mlp: MLP, scale: float
                                     ws.data_ptr(), ws.numel(), _stream(stream)),
            "qlora_mlp_backward")
     return dX, grads
+
+
+# --------------------------------------------------------------------------
+# Activation checkpoints in 8 bits, RMSNorm, products with any 4-bit format.
+# These calls run on the device of their tensors, whichever is current, and
+# check every buffer's size; what they allocate belongs to the stream they
+# run on.
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(t: torch.Tensor, stream):
+    """The context in which a call on t's device and `stream` allocates and
+    launches: the current stream of that device, or the given one (a
+    torch.cuda.Stream or a raw handle)."""
+    if stream is None:
+        return _HERE if t.device.index == torch._C._cuda_getDevice() else torch.cuda.device(t.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        h = int(stream)
+        stream = (torch.cuda.ExternalStream(h, device=t.device) if h
+                  else torch.cuda.default_stream(t.device))
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _raw_stream() -> int:
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _arg(t: torch.Tensor, dtype, shape, dev, name: str) -> int:
+    """Pointer of a contiguous tensor of this type, shape and device."""
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ' (not contiguous)'}")
+    return t.data_ptr()
+
+
+def _matrix(t: torch.Tensor, name: str):
+    """(rows, cols, device) of a contiguous 2-D bf16 CUDA tensor."""
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 2-D CUDA torch.bfloat16 tensor")
+    return t.shape[0], t.shape[1], t.device
+
+
+@dataclass
+class Act8:
+    """A blockwise 8-bit copy of a rows x cols bf16 activation: one code per
+    value (int8, or FP8 E4M3) and one fp32 scale per 64 values of a row."""
+    codes: torch.Tensor       # int8 or float8_e4m3fn [rows * cols]
+    scales: torch.Tensor      # float32 [rows * cols / 64]
+    rows: int
+    cols: int
+    code: int = QLORA_ACT8_INT8
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + 4 * self.scales.numel()
+
+    def c_struct(self, dev, name: str, rows=None, cols=None) -> _Act8:
+        r, c = self.rows, self.cols
+        if (rows is not None and r != rows) or (cols is not None and c != cols):
+            raise ValueError(f"{name} is {r} x {c}, expected {r if rows is None else rows} x "
+                             f"{c if cols is None else cols}")
+        for t, n, what in ((self.codes, r * c, "codes"), (self.scales, r * c // ACT8_BLOCK, "scales")):
+            if t.numel() != n or not t.is_contiguous() or not t.is_cuda or t.device != dev:
+                raise ValueError(f"{name}.{what} must be a contiguous tensor of {n} values on {dev}")
+        if self.codes.element_size() != 1 or self.scales.dtype != torch.float32:
+            raise ValueError(f"{name}: codes are one byte each, scales torch.float32")
+        return _Act8(self.codes.data_ptr(), self.scales.data_ptr(), r, c, self.code)
+
+
+def qlora_act8_sizes(rows: int, cols: int):
+    """(bytes of the codes, bytes of the scales) of a rows x cols copy."""
+    c, s = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().qlora_act8_sizes(rows, cols, ctypes.byref(c), ctypes.byref(s)), "qlora_act8_sizes")
+    return c.value, s.value
+
+
+def empty_act8(rows: int, cols: int, code: int = QLORA_ACT8_INT8, device="cuda") -> Act8:
+    if rows < 0 or cols < 0 or cols % ACT8_BLOCK:
+        qlora_act8_sizes(rows, cols)       # raises what the library says of these sizes
+    dt = torch.float8_e4m3fn if code == QLORA_ACT8_E4M3 else torch.int8
+    return Act8(torch.empty(rows * cols, dtype=dt, device=device),
+                torch.empty(rows * cols // ACT8_BLOCK, dtype=torch.float32, device=device), rows, cols, code)
+
+
+def qlora_act8_quantize(X: torch.Tensor, code: int = QLORA_ACT8_INT8, out: Act8 | None = None,
+                        stream=None) -> Act8:
+    """The 8-bit copy of a bf16 [rows, cols] activation (cols % 64 == 0), in
+    `out` with its code if given."""
+    M, K, dev = _matrix(X, "X")
+    with _on(X, stream):
+        out = out if out is not None else empty_act8(M, K, code, dev)
+        st = out.c_struct(dev, "out", M, K)
+        _check(lib().qlora_act8_quantize(X.data_ptr(), st, _raw_stream()), "qlora_act8_quantize")
+    return out
+
+
+def qlora_act8_dequantize(x8: Act8, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The bf16 values of an 8-bit copy."""
+    dev = x8.codes.device
+    with _on(x8.codes, stream):
+        if out is None:
+            out = torch.empty(x8.rows, x8.cols, dtype=torch.bfloat16, device=dev)
+        _check(lib().qlora_act8_dequantize(x8.c_struct(dev, "x8"),
+                                           _arg(out, torch.bfloat16, (x8.rows, x8.cols), dev, "out"),
+                                           _raw_stream()), "qlora_act8_dequantize")
+    return out
+
+
+def qlora_swiglu_forward_act8(G: torch.Tensor, U: torch.Tensor, code: int = QLORA_ACT8_INT8,
+                              H: torch.Tensor | None = None, g8: Act8 | None = None,
+                              u8: Act8 | None = None, stream=None):
+    """(H, g8, u8): H = silu(G) * U and the 8-bit copies its backward reads."""
+    M, F, dev = _matrix(G, "G")
+    with _on(G, stream):
+        pu = _arg(U, torch.bfloat16, G.shape, dev, "U")
+        H = H if H is not None else torch.empty_like(G)
+        g8 = g8 if g8 is not None else empty_act8(M, F, code, dev)
+        u8 = u8 if u8 is not None else empty_act8(M, F, g8.code, dev)
+        _check(lib().qlora_swiglu_forward_act8(G.data_ptr(), pu, _arg(H, torch.bfloat16, G.shape, dev, "H"),
+                                               g8.c_struct(dev, "g8", M, F), u8.c_struct(dev, "u8", M, F),
+                                               _raw_stream()), "qlora_swiglu_forward_act8")
+    return H, g8, u8
+
+
+def qlora_swiglu_backward_act8(dH: torch.Tensor, g8: Act8, u8: Act8, dG: torch.Tensor | None = None,
+                               dU: torch.Tensor | None = None, H: torch.Tensor | None = None,
+                               stream=None):
+    """(dG, dU) from the 8-bit copies; H, if given, receives silu(g~) * u~."""
+    M, F, dev = _matrix(dH, "dH")
+    with _on(dH, stream):
+        dG = dG if dG is not None else torch.empty_like(dH)
+        dU = dU if dU is not None else torch.empty_like(dH)
+        ph = None if H is None else _arg(H, torch.bfloat16, dH.shape, dev, "H")
+        _check(lib().qlora_swiglu_backward_act8(dH.data_ptr(), g8.c_struct(dev, "g8", M, F),
+                                                u8.c_struct(dev, "u8", M, F),
+                                                _arg(dG, torch.bfloat16, dH.shape, dev, "dG"),
+                                                _arg(dU, torch.bfloat16, dH.shape, dev, "dU"), ph,
+                                                _raw_stream()), "qlora_swiglu_backward_act8")
+    return dG, dU
+
+
+def _nf4_struct(w: NF4Tensor, dev, name: str) -> _Tensor:
+    p, c, m = qlora_quantized_sizes(w.rows, w.cols)
+    for t, n, what in ((w.packed, p, "packed"), (w.scale_codes, c, "scale_codes"),
+                       (w.meta_scale, m // 4, "meta_scale")):
+        if t.numel() < n or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name}.{what} must be a contiguous tensor of {n} values on {dev}")
+    return w.c_struct()
+
+
+def _workspace(ws, size: int, dev) -> torch.Tensor:
+    if ws is None:
+        return torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {dev}")
+    return ws
+
+
+def qlora_linear_backward_act8(dY: torch.Tensor, x8: Act8, w: NF4Tensor, A: torch.Tensor,
+                               B: torch.Tensor, scale: float, T_saved: torch.Tensor | None = None,
+                               dX: torch.Tensor | None = None, dA: torch.Tensor | None = None,
+                               dB: torch.Tensor | None = None, accumulate: bool = False,
+                               want_dX: bool = True, ws: torch.Tensor | None = None, stream=None):
+    """(dX, dA, dB) of the adapted layer from its input's 8-bit copy; dX is
+    None when want_dX is False."""
+    M, N, dev = _matrix(dY, "dY")
+    K, r = w.cols, A.shape[0]
+    bf, f32 = torch.bfloat16, torch.float32
+    if w.rows != N:
+        raise ValueError(f"dY has {N} columns, the weight {w.rows} rows")
+    with _on(dY, stream):
+        if not want_dX:
+            dX = None
+        elif dX is None:
+            dX = torch.empty(M, K, dtype=bf, device=dev)
+        if accumulate and (dA is None or dB is None):
+            raise ValueError("accumulate needs dA and dB")
+        dA = dA if dA is not None else torch.empty(r, K, dtype=f32, device=dev)
+        dB = dB if dB is not None else torch.empty(N, r, dtype=f32, device=dev)
+        ws = _workspace(ws, qlora_linear_workspace_size(M, N, K, r) if ws is None else 0, dev)
+        _check(lib().qlora_linear_backward_act8(
+            dY.data_ptr(), x8.c_struct(dev, "x8", M, K), _nf4_struct(w, dev, "w"),
+            _arg(A, bf, (r, K), dev, "A"), _arg(B, bf, (N, r), dev, "B"), r, float(scale),
+            None if T_saved is None else _arg(T_saved, f32, (M, r), dev, "T_saved"),
+            None if dX is None else _arg(dX, bf, (M, K), dev, "dX"), _arg(dA, f32, (r, K), dev, "dA"),
+            _arg(dB, f32, (N, r), dev, "dB"), int(bool(accumulate)), ws.data_ptr(), ws.nbytes,
+            _raw_stream()), "qlora_linear_backward_act8")
+    return dX, dA, dB
+
+
+@dataclass
+class MLPSaved8:
+    """What qlora_mlp_forward_act8 keeps: gate(x) and up(x) in 8 bits and the
+    three layers' X A^T in fp32 [M, r]."""
+    g: Act8
+    u: Act8
+    T_gate: torch.Tensor
+    T_up: torch.Tensor
+    T_down: torch.Tensor
+
+    @property
+    def nbytes(self) -> int:
+        return self.g.nbytes + self.u.nbytes + 3 * 4 * self.T_gate.numel()
+
+    def c_struct(self, dev, M: int, F: int, r: int) -> _MlpSaved8:
+        t = [_arg(getattr(self, n), torch.float32, (M, r), dev, n) for n in ("T_gate", "T_up", "T_down")]
+        return _MlpSaved8(self.g.c_struct(dev, "saved.g", M, F), self.u.c_struct(dev, "saved.u", M, F), *t)
+
+
+def empty_mlp_saved8(M: int, mlp: MLP, code: int = QLORA_ACT8_INT8, device="cuda") -> MLPSaved8:
+    t = [torch.empty(M, mlp.r, dtype=torch.float32, device=device) for _ in range(3)]
+    return MLPSaved8(empty_act8(M, mlp.gate.rows, code, device), empty_act8(M, mlp.gate.rows, code, device), *t)
+
+
+def _mlp_struct(mlp: MLP, dev) -> _Mlp:
+    for n in ("gate", "up", "down"):
+        w = getattr(mlp, n)
+        _nf4_struct(w, dev, n)
+        _arg(getattr(mlp, f"A_{n}"), torch.bfloat16, (mlp.r, w.cols), dev, f"A_{n}")
+        _arg(getattr(mlp, f"B_{n}"), torch.bfloat16, (w.rows, mlp.r), dev, f"B_{n}")
+    return mlp.c_struct()
+
+
+def qlora_mlp_forward_act8(X: torch.Tensor, mlp: MLP, scale: float, code: int = QLORA_ACT8_INT8,
+                           Y: torch.Tensor | None = None, saved: MLPSaved8 | None = None,
+                           ws: torch.Tensor | None = None, stream=None):
+    """(Y, saved): qlora_mlp_forward that also keeps what
+    qlora_mlp_backward_act8 reads, in 8 bits, instead of recomputing it."""
+    M, D, dev = _matrix(X, "X")
+    if D != mlp.gate.cols:
+        raise ValueError(f"X has {D} columns, gate {mlp.gate.cols}")
+    with _on(X, stream):
+        st = _mlp_struct(mlp, dev)
+        Y = Y if Y is not None else torch.empty_like(X)
+        saved = saved if saved is not None else empty_mlp_saved8(M, mlp, code, dev)
+        sv = saved.c_struct(dev, M, mlp.gate.rows, mlp.r)
+        ws = _workspace(ws, qlora_mlp_workspace_size(M, mlp) if ws is None else 0, dev)
+        _check(lib().qlora_mlp_forward_act8(X.data_ptr(), st, float(scale),
+                                            _arg(Y, torch.bfloat16, X.shape, dev, "Y"), sv, ws.data_ptr(),
+                                            ws.nbytes, _raw_stream()), "qlora_mlp_forward_act8")
+    return Y, saved
+
+
+def qlora_mlp_backward_act8(dY: torch.Tensor, x8: Act8, mlp: MLP, scale: float, saved: MLPSaved8,
+                            dX: torch.Tensor | None = None, grads: dict | None = None,
+                            accumulate: bool = False, ws: torch.Tensor | None = None, stream=None):
+    """(dX, grads) as qlora_mlp_backward, from the 8-bit copies of X, gate(X)
+    and up(X): nothing is recomputed through the weights."""
+    M, D, dev = _matrix(dY, "dY")
+    if D != mlp.gate.cols:
+        raise ValueError(f"dY has {D} columns, gate {mlp.gate.cols}")
+    f32, names = torch.float32, ("gate", "up", "down")
+    with _on(dY, stream):
+        st = _mlp_struct(mlp, dev)
+        dX = dX if dX is not None else torch.empty_like(dY)
+        if grads is None:
+            if accumulate:
+                raise ValueError("accumulate needs grads")
+            grads = {}
+            for n in names:
+                w = getattr(mlp, n)
+                grads[f"dA_{n}"] = torch.empty(mlp.r, w.cols, dtype=f32, device=dev)
+                grads[f"dB_{n}"] = torch.empty(w.rows, mlp.r, dtype=f32, device=dev)
+        g = []
+        for n in names:
+            w = getattr(mlp, n)
+            g += [_arg(grads[f"dA_{n}"], f32, (mlp.r, w.cols), dev, f"dA_{n}"),
+                  _arg(grads[f"dB_{n}"], f32, (w.rows, mlp.r), dev, f"dB_{n}")]
+        sv = saved.c_struct(dev, M, mlp.gate.rows, mlp.r)
+        ws = _workspace(ws, qlora_mlp_workspace_size(M, mlp) if ws is None else 0, dev)
+        _check(lib().qlora_mlp_backward_act8(dY.data_ptr(), x8.c_struct(dev, "x8", M, D), st, float(scale), sv,
+                                             _arg(dX, torch.bfloat16, dY.shape, dev, "dX"), _MlpGrads(*g),
+                                             int(bool(accumulate)), ws.data_ptr(), ws.nbytes, _raw_stream()),
+               "qlora_mlp_backward_act8")
+    return dX, grads
+
+
+def qlora_rmsnorm_forward(X: torch.Tensor, weight: torch.Tensor, eps: float,
+                          residual: torch.Tensor | None = None, H: torch.Tensor | None = None,
+                          Y: torch.Tensor | None = None, q8: Act8 | None = None, want_Y: bool = True,
+                          stream=None):
+    """(Y, H): H = X + residual in bf16 (X itself without a residual) and
+    Y = H / rms(H) * weight, weight fp32.  q8, if given, receives Y's 8-bit
+    copy; with want_Y False only that is written and Y is None."""
+    M, D, dev = _matrix(X, "X")
+    bf = torch.bfloat16
+    with _on(X, stream):
+        pw = _arg(weight, torch.float32, (D,), dev, "weight")
+        pr = None if residual is None else _arg(residual, bf, X.shape, dev, "residual")
+        if H is None and residual is not None:
+            H = torch.empty_like(X)
+        if not want_Y:
+            Y = None
+        elif Y is None:
+            Y = torch.empty_like(X)
+        _check(lib().qlora_rmsnorm_forward(
+            X.data_ptr(), pr, pw, M, D, eps, None if H is None else _arg(H, bf, X.shape, dev, "H"),
+            None if Y is None else _arg(Y, bf, X.shape, dev, "Y"),
+            None if q8 is None else q8.c_struct(dev, "q8", M, D), _raw_stream()), "qlora_rmsnorm_forward")
+    return Y, (X if H is None else H)
+
+
+def qlora_rmsnorm_workspace_size(M: int, D: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().qlora_rmsnorm_workspace_size(M, D, ctypes.byref(b)), "qlora_rmsnorm_workspace_size")
+    return b.value
+
+
+def qlora_rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Tensor, eps: float,
+                           dres: torch.Tensor | None = None, dX: torch.Tensor | None = None,
+                           dweight: torch.Tensor | None = None, want_dweight: bool = True,
+                           accumulate: bool = False, ws: torch.Tensor | None = None, stream=None):
+    """(dX, dweight): dX is the gradient of X and of the residual alike, dres
+    the gradient that reaches H past the norm; dweight (fp32) is None when
+    want_dweight is False (a frozen norm)."""
+    M, D, dev = _matrix(dY, "dY")
+    bf, f32 = torch.bfloat16, torch.float32
+    with _on(dY, stream):
+        ph = _arg(H, bf, dY.shape, dev, "H")
+        pw = _arg(weight, f32, (D,), dev, "weight")
+        pr = None if dres is None else _arg(dres, bf, dY.shape, dev, "dres")
+        dX = dX if dX is not None else torch.empty_like(dY)
+        if not want_dweight:
+            dweight = None
+        elif dweight is None:
+            if accumulate:
+                raise ValueError("accumulate needs dweight")
+            dweight = torch.empty(D, dtype=f32, device=dev)
+        if dweight is not None:
+            ws = _workspace(ws, qlora_rmsnorm_workspace_size(M, D) if ws is None else 0, dev)
+        _check(lib().qlora_rmsnorm_backward(
+            dY.data_ptr(), ph, pr, pw, M, D, eps, _arg(dX, bf, dY.shape, dev, "dX"),
+            None if dweight is None else _arg(dweight, f32, (D,), dev, "dweight"), int(bool(accumulate)),
+            None if dweight is None else ws.data_ptr(), 0 if dweight is None else ws.nbytes, _raw_stream()),
+            "qlora_rmsnorm_backward")
+    return dX, dweight

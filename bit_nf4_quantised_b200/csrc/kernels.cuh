@@ -165,6 +165,8 @@ int gemm_col_granule(bool trans);
 //   q_kmajor: Q stored [J][C] (ld = ldq) else [C][J].
 //   err_zero: if set, one thread stores 0 there (clears the call's error word).
 constexpr int kMaxSkinnySplits = 8;
+//   P8, Pscale, p_code: P in blockwise 8 bits instead (P8 != null, P unused;
+//             q_kmajor == p_kmajor; ldp a multiple of 64 and, K-major, so is C)
 struct SkinnyArgs {
     const uint16_t* P;
     const uint16_t* Q;
@@ -187,6 +189,9 @@ struct SkinnyArgs {
     int programmatic;         // launch as the previous kernel's programmatic dependent; the
                               // kernel never waits for that grid, so its inputs must come
                               // from earlier work
+    const uint8_t* P8;
+    const float* Pscale;
+    int p_code;               // a qlora_act8_code
 };
 cudaError_t launch_skinny(bool p_kmajor, bool q_kmajor, const SkinnyArgs& a, cudaStream_t stream);
 
@@ -245,5 +250,52 @@ cudaError_t launch_add_bf16(const uint16_t* A, const uint16_t* B, uint16_t* C, i
                             int num_sms, cudaStream_t s);
 cudaError_t launch_or_words(int* dst, const int* a, const int* b, const int* c, bool accumulate,
                             cudaStream_t s);
+
+// ------------------------------------- activation checkpoints in 8 bits
+// n = elements, a multiple of 64 (act8.cuh has the format)
+struct Act8View {
+    uint8_t* codes;
+    float* scales;
+    int code;                  // a qlora_act8_code
+};
+cudaError_t launch_act8_quantize(const uint16_t* X, const Act8View& o, int64_t n, int num_sms, cudaStream_t s);
+cudaError_t launch_act8_dequantize(const Act8View& v, uint16_t* X, int64_t n, int num_sms, cudaStream_t s);
+// H = bf16(silu(G) U) and the 8-bit copies of G and U (one code for both)
+cudaError_t launch_swiglu_forward_act8(const uint16_t* G, const uint16_t* U, uint16_t* H, const Act8View& g,
+                                       const Act8View& u, int64_t n, int num_sms, cudaStream_t s);
+// from the copies: (dG, dU) if dG is given, H if H is given (at least one)
+cudaError_t launch_swiglu_backward_act8(const uint16_t* dH, const Act8View& g, const Act8View& u, uint16_t* dG,
+                                        uint16_t* dU, uint16_t* H, int64_t n, int num_sms, cudaStream_t s);
+
+// ------------------------------------------------- RMSNorm with a residual
+struct RmsNormArgs {
+    const uint16_t* X;
+    const uint16_t* R;         // nullable: h = bf16(x + r)
+    const float* weight;
+    uint16_t* H;               // nullable: h
+    uint16_t* Y;               // nullable
+    Act8View q;                // q.codes nullable: y's 8-bit copy
+    int64_t M;
+    int D;                     // a multiple of 8; of 64 with q
+    float eps;
+};
+cudaError_t launch_rmsnorm_forward(const RmsNormArgs& a, int num_sms, cudaStream_t s);
+
+struct RmsNormGradArgs {
+    const uint16_t* dY;
+    const uint16_t* H;
+    const uint16_t* dR;        // nullable: gradient that reaches h past the norm
+    const float* weight;
+    uint16_t* dX;
+    float* dweight;            // nullable
+    int accumulate;
+    float* part;               // [parts][D] fp32, parts = rmsnorm_parts(M, D, num_sms)
+    int64_t M;
+    int D;
+    float eps;
+};
+int rmsnorm_max_width();
+int rmsnorm_parts(int64_t M, int D, int num_sms);
+cudaError_t launch_rmsnorm_backward(const RmsNormGradArgs& a, int num_sms, cudaStream_t s);
 
 }  // namespace qnf4

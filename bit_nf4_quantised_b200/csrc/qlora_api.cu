@@ -342,6 +342,29 @@ int check_format(const qlora_format* f, FmtTable* t, FmtArgs* a) {
     return QLORA_OK;
 }
 
+// An 8-bit activation copy: sizes, code and buffers (which may be NULL when
+// it is empty).  *v gets what the kernels take.
+int check_act8(const qlora_act8* x, Act8View* v) {
+    if (!x) return QLORA_ERR_NULL;
+    if (x->rows < 0 || x->cols < 0 || (x->cols > 0 && x->rows > INT64_MAX / 2 / x->cols)) return QLORA_ERR_SHAPE;
+    if (x->cols % 64 != 0) return QLORA_ERR_UNSUPPORTED;
+    if (x->code != QLORA_ACT8_INT8 && x->code != QLORA_ACT8_E4M3) return QLORA_ERR_UNSUPPORTED;
+    if (x->rows > 0 && x->cols > 0 && (!x->codes || !x->scales)) return QLORA_ERR_NULL;
+    if (!aligned(x->codes, 16) || !aligned(x->scales, 16)) return QLORA_ERR_ALIGN;
+    v->codes = static_cast<uint8_t*>(x->codes);
+    v->scales = x->scales;
+    v->code = x->code;
+    return QLORA_OK;
+}
+
+// Two copies of the same sizes and code, as the SwiGLU takes them.
+int check_act8_pair(const qlora_act8* a, const qlora_act8* b, Act8View* va, Act8View* vb) {
+    int st = check_act8(a, va);
+    if (st == QLORA_OK) st = check_act8(b, vb);
+    if (st != QLORA_OK) return st;
+    return a->rows == b->rows && a->cols == b->cols && a->code == b->code ? QLORA_OK : QLORA_ERR_SHAPE;
+}
+
 // Bound of the tensor-core GEMM's operational waits (qlora_set_gemm_wait_limit_us).
 std::atomic<unsigned long long> g_gemm_wait_ns{kWaitLimitNs};
 
@@ -400,12 +423,21 @@ SkinnyArgs skinny_args(const uint16_t* P, const uint16_t* Q, int64_t I, int64_t 
     return a;
 }
 
-// T = X A^T -> optional fp32 T_save and bf16 gamma*T padded to rp columns.
+// P from an 8-bit copy instead of bf16.
+void take_act8(SkinnyArgs& a, const Act8View& x) {
+    a.P8 = x.codes;
+    a.Pscale = x.scales;
+    a.p_code = x.code;
+}
+
+// T = X A^T -> optional fp32 T_save and bf16 gamma*T padded to rp columns
+// (X in bf16, or NULL and its 8-bit copy).
 // trigger: a GEMM launched next as its programmatic dependent may start at once.
-cudaError_t run_T(const uint16_t* X, const uint16_t* A, int64_t M, int64_t K, int r, float gamma,
-                  float* T_save, uint16_t* Gt, int64_t rp, int* err_zero, bool trigger,
-                  cudaStream_t s) {
+cudaError_t run_T(const uint16_t* X, const Act8View& x8, const uint16_t* A, int64_t M, int64_t K,
+                  int r, float gamma, float* T_save, uint16_t* Gt, int64_t rp, int* err_zero,
+                  bool trigger, cudaStream_t s) {
     SkinnyArgs a = skinny_args(X, A, M, r, K, K, K);
+    if (!X) take_act8(a, x8);
     a.out = T_save;
     a.out_bf16 = Gt;
     a.ldb = rp;
@@ -788,7 +820,7 @@ int qlora_linear_forward_ex(const uint16_t* X, int64_t M, const qlora_nf4_tensor
         QTRY(launch_gemv_finalize(f, s));
         return QLORA_OK;
     }
-    QTRY(run_T(X, A, M, K, r, scale, T_save, Gt, p.rp, err, true, s));
+    QTRY(run_T(X, Act8View{}, A, M, K, r, scale, T_save, Gt, p.rp, err, true, s));
 
     // B [N x r] is read in place: the 64-wide TMA box zero-fills columns >= r
     CUtensorMap m_act, m_packed, m_la, m_lb, m_out;
@@ -833,12 +865,18 @@ int qlora_linear_forward(const uint16_t* X, int64_t M, const qlora_nf4_tensor* w
                                    nullptr);
 }
 
-int qlora_linear_backward_ex(const uint16_t* dY, const uint16_t* X, int64_t M,
-                             const qlora_nf4_tensor* w, const uint16_t* A, const uint16_t* B,
-                             int r, float scale, const float* T_saved, uint16_t* dX, float* dA,
-                             float* dB, int accumulate, void* ws, size_t ws_bytes,
-                             qlora_stream_t stream, const qlora_events* ev) {
-    if (!A || !B || !dA || !dB || (M != 0 && (!dY || !X))) return QLORA_ERR_NULL;
+}  // extern "C"
+
+namespace {
+
+// The backward of one adapted layer from X in bf16 or, with X NULL, from its
+// 8-bit copy x8 (checked by the caller; null codes when M = 0).
+int linear_backward(const uint16_t* dY, const uint16_t* X, const Act8View& x8, int64_t M,
+                    const qlora_nf4_tensor* w, const uint16_t* A, const uint16_t* B, int r,
+                    float scale, const float* T_saved, uint16_t* dX, float* dA, float* dB,
+                    int accumulate, void* ws, size_t ws_bytes, qlora_stream_t stream,
+                    const qlora_events* ev) {
+    if (!A || !B || !dA || !dB || (M != 0 && (!dY || (!X && !x8.codes)))) return QLORA_ERR_NULL;
     int st = check_tensor(w);
     if (st != QLORA_OK) return st;
     const int64_t N = w->rows, K = w->cols;
@@ -866,7 +904,7 @@ int qlora_linear_backward_ex(const uint16_t* dY, const uint16_t* X, int64_t M,
     int* err_first = err;                 // cleared by the first kernel of the call
 
     if (!T_saved) {                       // recompute gamma * T in bf16
-        QTRY(run_T(X, A, M, K, r, scale, nullptr, Gt, p.rp, err_first, false, s));
+        QTRY(run_T(X, x8, A, M, K, r, scale, nullptr, Gt, p.rp, err_first, false, s));
         err_first = nullptr;
     }
     // U = dY B -> gamma * U in bf16; converts a saved T to gamma * T on the side
@@ -934,6 +972,7 @@ int qlora_linear_backward_ex(const uint16_t* dY, const uint16_t* X, int64_t M,
     }
     {
         SkinnyArgs a = skinny_args(X, Gu, K, r, M, K, p.rp);
+        if (!X) take_act8(a, x8);
         a.out = dA;
         a.transpose = 1;
         a.accumulate = accumulate;
@@ -941,6 +980,19 @@ int qlora_linear_backward_ex(const uint16_t* dY, const uint16_t* X, int64_t M,
         QTRY(launch_skinny(false, false, a, s));
     }
     return QLORA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qlora_linear_backward_ex(const uint16_t* dY, const uint16_t* X, int64_t M,
+                             const qlora_nf4_tensor* w, const uint16_t* A, const uint16_t* B,
+                             int r, float scale, const float* T_saved, uint16_t* dX, float* dA,
+                             float* dB, int accumulate, void* ws, size_t ws_bytes,
+                             qlora_stream_t stream, const qlora_events* ev) {
+    return linear_backward(dY, X, Act8View{}, M, w, A, B, r, scale, T_saved, dX, dA, dB, accumulate,
+                           ws, ws_bytes, stream, ev);
 }
 
 int qlora_linear_backward(const uint16_t* dY, const uint16_t* X, int64_t M,
@@ -1121,6 +1173,256 @@ int qlora_mlp_backward(const uint16_t* dY, const uint16_t* X, int64_t M, const q
     QTRY(launch_or_words(at<int>(ws, 0), at<int>(ws, p.off_lin[3]), at<int>(ws, p.off_lin[4]),
                          at<int>(ws, p.off_lin[4]), true, s));
     return QLORA_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------- activation checkpoints in 8 bits, RMSNorm
+namespace {
+
+// saved copies of an MLP's M x F activations; *M from them
+int check_saved8(const qlora_mlp* mlp, const qlora_mlp_saved8* sv, Act8View* g, Act8View* u, int64_t* M) {
+    if (!mlp || !sv) return QLORA_ERR_NULL;
+    const int st = check_act8_pair(&sv->g, &sv->u, g, u);
+    if (st != QLORA_OK) return st;
+    if (sv->g.cols != mlp->gate.rows) return QLORA_ERR_SHAPE;
+    *M = sv->g.rows;
+    if (*M != 0 && (!sv->T_gate || !sv->T_up || !sv->T_down)) return QLORA_ERR_NULL;
+    if (!aligned(sv->T_gate, 16) || !aligned(sv->T_up, 16) || !aligned(sv->T_down, 16)) return QLORA_ERR_ALIGN;
+    return QLORA_OK;
+}
+
+int check_rmsnorm(int64_t M, int64_t D, float eps) {
+    if (M < 0 || D < 0) return QLORA_ERR_SHAPE;
+    if (D < 8 || D % 8 != 0 || D > rmsnorm_max_width() || M > INT64_MAX / 8 / D) return QLORA_ERR_UNSUPPORTED;
+    if (!std::isfinite(eps) || eps < 0.f) return QLORA_ERR_UNSUPPORTED;
+    return QLORA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qlora_act8_sizes(int64_t rows, int64_t cols, size_t* code_bytes, size_t* scale_bytes) {
+    if (!code_bytes || !scale_bytes) return QLORA_ERR_NULL;
+    if (rows < 0 || cols < 0 || (cols > 0 && rows > INT64_MAX / 2 / cols)) return QLORA_ERR_SHAPE;
+    if (cols % 64 != 0) return QLORA_ERR_UNSUPPORTED;
+    *code_bytes = static_cast<size_t>(rows * cols);
+    *scale_bytes = static_cast<size_t>(rows * cols / 64) * 4;
+    return QLORA_OK;
+}
+
+int qlora_act8_quantize(const uint16_t* X, const qlora_act8* out, qlora_stream_t stream) {
+    Act8View v;
+    const int st = check_act8(out, &v);
+    if (st != QLORA_OK) return st;
+    const int64_t n = out->rows * out->cols;
+    if (n == 0) return QLORA_OK;
+    if (!X) return QLORA_ERR_NULL;
+    if (!aligned(X, 16)) return QLORA_ERR_ALIGN;
+    return cuda_status(launch_act8_quantize(X, v, n, num_sms(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qlora_act8_dequantize(const qlora_act8* x, uint16_t* X_out, qlora_stream_t stream) {
+    Act8View v;
+    const int st = check_act8(x, &v);
+    if (st != QLORA_OK) return st;
+    const int64_t n = x->rows * x->cols;
+    if (n == 0) return QLORA_OK;
+    if (!X_out) return QLORA_ERR_NULL;
+    if (!aligned(X_out, 16)) return QLORA_ERR_ALIGN;
+    return cuda_status(launch_act8_dequantize(v, X_out, n, num_sms(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qlora_swiglu_forward_act8(const uint16_t* G, const uint16_t* U, uint16_t* H, const qlora_act8* g8,
+                              const qlora_act8* u8, qlora_stream_t stream) {
+    Act8View g, u;
+    const int st = check_act8_pair(g8, u8, &g, &u);
+    if (st != QLORA_OK) return st;
+    const int64_t n = g8->rows * g8->cols;
+    if (n == 0) return QLORA_OK;
+    if (!G || !U || !H) return QLORA_ERR_NULL;
+    if (!aligned(G, 16) || !aligned(U, 16) || !aligned(H, 16)) return QLORA_ERR_ALIGN;
+    return cuda_status(launch_swiglu_forward_act8(G, U, H, g, u, n, num_sms(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qlora_swiglu_backward_act8(const uint16_t* dH, const qlora_act8* g8, const qlora_act8* u8, uint16_t* dG,
+                               uint16_t* dU, uint16_t* H, qlora_stream_t stream) {
+    Act8View g, u;
+    const int st = check_act8_pair(g8, u8, &g, &u);
+    if (st != QLORA_OK) return st;
+    const int64_t n = g8->rows * g8->cols;
+    if (n == 0) return QLORA_OK;
+    if (!dH || !dG || !dU) return QLORA_ERR_NULL;
+    if (!aligned(dH, 16) || !aligned(dG, 16) || !aligned(dU, 16) || !aligned(H, 16)) return QLORA_ERR_ALIGN;
+    return cuda_status(launch_swiglu_backward_act8(dH, g, u, dG, dU, H, n, num_sms(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qlora_linear_backward_act8(const uint16_t* dY, const qlora_act8* x8, const qlora_nf4_tensor* w,
+                               const uint16_t* A, const uint16_t* B, int r, float scale,
+                               const float* T_saved, uint16_t* dX, float* dA, float* dB, int accumulate,
+                               void* ws, size_t ws_bytes, qlora_stream_t stream) {
+    Act8View v;
+    const int st = check_act8(x8, &v);
+    if (st != QLORA_OK) return st;
+    if (!w) return QLORA_ERR_NULL;
+    if (x8->cols != w->cols) return QLORA_ERR_SHAPE;
+    return linear_backward(dY, nullptr, v, x8->rows, w, A, B, r, scale, T_saved, dX, dA, dB, accumulate, ws,
+                           ws_bytes, stream, nullptr);
+}
+
+int qlora_mlp_forward_act8(const uint16_t* X, const qlora_mlp* mlp, float scale, uint16_t* Y,
+                           const qlora_mlp_saved8* saved, void* ws, size_t ws_bytes, qlora_stream_t stream) {
+    Act8View g8, u8;
+    int64_t M = 0;
+    int st = check_saved8(mlp, saved, &g8, &u8, &M);
+    if (st != QLORA_OK) return st;
+    MlpPlan p;
+    st = mlp_plan(M, mlp, &p);
+    if (st == QLORA_OK) st = check_mlp_adapters(mlp);
+    if (st != QLORA_OK) return st;
+    if (M != 0 && (!X || !Y)) return QLORA_ERR_NULL;
+    if (!aligned(X, 16) || !aligned(Y, 16)) return QLORA_ERR_ALIGN;
+    if (!ws || ws_bytes < static_cast<size_t>(p.total)) return QLORA_ERR_WORKSPACE;
+    if (!aligned(ws, kAlign)) return QLORA_ERR_ALIGN;
+    if (M == 0) return QLORA_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint16_t* G = at<uint16_t>(ws, p.off_g);
+    uint16_t* U = at<uint16_t>(ws, p.off_u);
+    uint16_t* H = at<uint16_t>(ws, p.off_h);
+    const int r = mlp->r;
+    st = qlora_linear_forward(X, M, &mlp->gate, mlp->A_gate, mlp->B_gate, r, scale, G, saved->T_gate,
+                              at<void>(ws, p.off_lin[0]), p.lin, stream);
+    if (st == QLORA_OK)
+        st = qlora_linear_forward(X, M, &mlp->up, mlp->A_up, mlp->B_up, r, scale, U, saved->T_up,
+                                  at<void>(ws, p.off_lin[1]), p.lin, stream);
+    if (st != QLORA_OK) return st;
+    QTRY(launch_swiglu_forward_act8(G, U, H, g8, u8, M * p.F, num_sms(), s));
+    st = qlora_linear_forward(H, M, &mlp->down, mlp->A_down, mlp->B_down, r, scale, Y, saved->T_down,
+                              at<void>(ws, p.off_lin[2]), p.lin, stream);
+    if (st != QLORA_OK) return st;
+    QTRY(launch_or_words(at<int>(ws, 0), at<int>(ws, p.off_lin[0]), at<int>(ws, p.off_lin[1]),
+                         at<int>(ws, p.off_lin[2]), false, s));
+    return QLORA_OK;
+}
+
+int qlora_mlp_backward_act8(const uint16_t* dY, const qlora_act8* x8, const qlora_mlp* mlp, float scale,
+                            const qlora_mlp_saved8* saved, uint16_t* dX, const qlora_mlp_grads* g,
+                            int accumulate, void* ws, size_t ws_bytes, qlora_stream_t stream) {
+    Act8View xv, g8, u8;
+    int64_t M = 0;
+    int st = check_act8(x8, &xv);
+    if (st == QLORA_OK) st = check_saved8(mlp, saved, &g8, &u8, &M);
+    if (st != QLORA_OK) return st;
+    if (x8->rows != M || x8->cols != mlp->gate.cols) return QLORA_ERR_SHAPE;
+    // an empty batch reads no activation: its gradients are those of the
+    // recomputing backward
+    if (M == 0) return qlora_mlp_backward(dY, nullptr, 0, mlp, scale, dX, g, accumulate, ws, ws_bytes, stream);
+    MlpPlan p;
+    st = mlp_plan(M, mlp, &p);
+    if (st == QLORA_OK) st = check_mlp_adapters(mlp);
+    if (st != QLORA_OK) return st;
+    if (!g || !g->dA_gate || !g->dB_gate || !g->dA_up || !g->dB_up || !g->dA_down || !g->dB_down)
+        return QLORA_ERR_NULL;
+    if (!dY || !dX) return QLORA_ERR_NULL;
+    for (const float* t : {g->dA_gate, g->dB_gate, g->dA_up, g->dB_up, g->dA_down, g->dB_down})
+        if (!aligned(t, 16)) return QLORA_ERR_ALIGN;
+    if (!aligned(dY, 16) || !aligned(dX, 16)) return QLORA_ERR_ALIGN;
+    if (!ws || ws_bytes < static_cast<size_t>(p.total)) return QLORA_ERR_WORKSPACE;
+    if (!aligned(ws, kAlign)) return QLORA_ERR_ALIGN;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint16_t* G = at<uint16_t>(ws, p.off_g);
+    uint16_t* U = at<uint16_t>(ws, p.off_u);
+    uint16_t* H = at<uint16_t>(ws, p.off_h);
+    uint16_t* dH = at<uint16_t>(ws, p.off_dh);
+    uint16_t* dXg = at<uint16_t>(ws, p.off_dxg);
+    const int r = mlp->r, sms = num_sms();
+    const int64_t n = M * p.F;
+    // h~ for dA_down; then down's backward, the SwiGLU's, gate's and up's
+    QTRY(launch_swiglu_backward_act8(nullptr, g8, u8, nullptr, nullptr, H, n, sms, s));
+    st = qlora_linear_backward(dY, H, M, &mlp->down, mlp->A_down, mlp->B_down, r, scale, saved->T_down, dH,
+                               g->dA_down, g->dB_down, accumulate, at<void>(ws, p.off_lin[2]), p.lin, stream);
+    if (st != QLORA_OK) return st;
+    QTRY(launch_swiglu_backward_act8(dH, g8, u8, G, U, nullptr, n, sms, s));
+    st = linear_backward(G, nullptr, xv, M, &mlp->gate, mlp->A_gate, mlp->B_gate, r, scale, saved->T_gate, dXg,
+                         g->dA_gate, g->dB_gate, accumulate, at<void>(ws, p.off_lin[3]), p.lin, stream, nullptr);
+    if (st == QLORA_OK)
+        st = linear_backward(U, nullptr, xv, M, &mlp->up, mlp->A_up, mlp->B_up, r, scale, saved->T_up, dX,
+                             g->dA_up, g->dB_up, accumulate, at<void>(ws, p.off_lin[4]), p.lin, stream, nullptr);
+    if (st != QLORA_OK) return st;
+    QTRY(launch_add_bf16(dX, dXg, dX, M * p.D, sms, s));
+    QTRY(launch_or_words(at<int>(ws, 0), at<int>(ws, p.off_lin[2]), at<int>(ws, p.off_lin[3]),
+                         at<int>(ws, p.off_lin[4]), false, s));
+    return QLORA_OK;
+}
+
+int qlora_rmsnorm_forward(const uint16_t* X, const uint16_t* R, const float* weight, int64_t M, int64_t D,
+                          float eps, uint16_t* H, uint16_t* Y, const qlora_act8* y8, qlora_stream_t stream) {
+    int st = check_rmsnorm(M, D, eps);
+    if (st != QLORA_OK) return st;
+    if (!weight || (!Y && !y8 && M != 0)) return QLORA_ERR_NULL;
+    RmsNormArgs a{};
+    if (y8) {
+        st = check_act8(y8, &a.q);
+        if (st != QLORA_OK) return st;
+        if (y8->rows != M || y8->cols != D) return QLORA_ERR_SHAPE;
+    }
+    if (M == 0) return QLORA_OK;
+    if (!X) return QLORA_ERR_NULL;
+    if (!aligned(X, 16) || !aligned(R, 16) || !aligned(weight, 16) || !aligned(H, 16) || !aligned(Y, 16))
+        return QLORA_ERR_ALIGN;
+    a.X = X;
+    a.R = R;
+    a.weight = weight;
+    a.H = H;
+    a.Y = Y;
+    a.M = M;
+    a.D = static_cast<int>(D);
+    a.eps = eps;
+    return cuda_status(launch_rmsnorm_forward(a, num_sms(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qlora_rmsnorm_workspace_size(int64_t M, int64_t D, size_t* bytes) {
+    if (!bytes) return QLORA_ERR_NULL;
+    const int st = check_rmsnorm(M, D, 0.f);
+    if (st != QLORA_OK) return st;
+    *bytes = M == 0 ? 0 : static_cast<size_t>(rmsnorm_parts(M, static_cast<int>(D), num_sms())) * D * 4;
+    return QLORA_OK;
+}
+
+int qlora_rmsnorm_backward(const uint16_t* dY, const uint16_t* H, const uint16_t* dR, const float* weight,
+                           int64_t M, int64_t D, float eps, uint16_t* dX, float* dweight, int accumulate,
+                           void* ws, size_t ws_bytes, qlora_stream_t stream) {
+    int st = check_rmsnorm(M, D, eps);
+    if (st != QLORA_OK) return st;
+    if (!weight || (M != 0 && (!dY || !H || !dX))) return QLORA_ERR_NULL;
+    if (!aligned(dY, 16) || !aligned(H, 16) || !aligned(dR, 16) || !aligned(weight, 16) || !aligned(dX, 16) ||
+        !aligned(dweight, 16))
+        return QLORA_ERR_ALIGN;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (M == 0) {
+        if (dweight && !accumulate) QTRY(cudaMemsetAsync(dweight, 0, size_t(D) * 4, s));
+        return QLORA_OK;
+    }
+    const int sms = num_sms();
+    if (dweight) {
+        const size_t need = static_cast<size_t>(rmsnorm_parts(M, static_cast<int>(D), sms)) * D * 4;
+        if (!ws || ws_bytes < need) return QLORA_ERR_WORKSPACE;
+        if (!aligned(ws, kAlign)) return QLORA_ERR_ALIGN;
+    }
+    RmsNormGradArgs a{};
+    a.dY = dY;
+    a.H = H;
+    a.dR = dR;
+    a.weight = weight;
+    a.dX = dX;
+    a.dweight = dweight;
+    a.accumulate = accumulate;
+    a.part = static_cast<float*>(ws);
+    a.M = M;
+    a.D = static_cast<int>(D);
+    a.eps = eps;
+    return cuda_status(launch_rmsnorm_backward(a, sms, s));
 }
 
 }  // extern "C"

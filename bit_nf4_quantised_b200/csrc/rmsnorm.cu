@@ -1,0 +1,396 @@
+// RMSNorm in front of an adapted layer, with the residual's addition:
+//   h = bf16(x + r),  y = bf16(h rstd w),  rstd = 1 / sqrt(mean(h^2) + eps)
+// and, in the same pass, y's blockwise 8-bit copy (act8.cuh) for the layer's
+// backward.  The norm's weight is fp32 ("QLoRA, explained", "Failure modes",
+// "Silent fp32 casts": preparing a model for k-bit training casts its norms
+// to fp32).  Backward, with t = w dy:
+//   dx = rstd (t - h rstd^2 mean(h t)) + dr,   dw = sum over rows of dy h rstd
+// rstd is formed again from h, which the backward reads anyway, in the same
+// reduction as mean(h t): nothing but h is kept from the forward.
+//
+// Both directions are streams bounded by HBM: forward 2 + 2 (+2) bytes read
+// and 2 + 2 (+1 1/16) written per element, backward 4 (+2) read, 2 written.
+// A row lives in registers (8 bf16 a lane and 16-byte word, NV words a lane),
+// so each tensor crosses HBM once.  Rows of up to 1024 values belong to a
+// warp, longer ones to a CTA.  The grid is persistent: a lane keeps its
+// columns of w (and of dw) in registers over all its rows, and the loads of
+// the next row are issued before the reduction of the current one.
+#include "act8.cuh"
+
+namespace qnf4 {
+
+namespace {
+
+constexpr int kWarpRowMax = 1024;      // widest row that a single warp takes
+constexpr int kWarpRows = 8;           // warps (rows) of such a CTA
+constexpr int kMaxWidth = 16384;       // 512 lanes x 4 words x 8 values
+
+// Threads of the largest CTA that holds NV words of a row per lane.
+constexpr int max_threads(int nv) { return nv == 1 ? 1024 : 512; }
+
+__device__ __forceinline__ uint4 ldg_stream(const uint16_t* p) {
+    return __ldcs(reinterpret_cast<const uint4*>(p));
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Sum over the row's warps, in warp order; buf holds one float per warp and
+// alternates between two buffers, so one barrier per row is enough.
+__device__ __forceinline__ float row_sum(float v, float* buf, int nwarps) {
+    v = warp_sum(v);
+    if (nwarps == 1) return v;
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float s = 0.f;
+    for (int i = 0; i < nwarps; ++i) s += buf[i];
+    return s;
+}
+
+template <int NV, bool kRes, int kCode>      // kCode < 0: no 8-bit copy
+__global__ void __launch_bounds__(max_threads(NV))
+rmsnorm_forward_kernel(RmsNormArgs a) {
+    __shared__ float red[2][32];
+    const int nvec = a.D / 8, lanes = blockDim.x, nwarps = lanes / 32;
+    const int64_t stride = int64_t(gridDim.x) * blockDim.y;
+    int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    const float inv_d = 1.0f / static_cast<float>(a.D);
+
+    float w[NV][8];
+    uint4 x[NV], r[NV];
+    auto load = [&](int64_t m) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int v = threadIdx.x + k * lanes;
+            x[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (kRes) r[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (m < a.M && v < nvec) {
+                x[k] = ldg_stream(a.X + m * a.D + v * 8);
+                if (kRes) r[k] = ldg_stream(a.R + m * a.D + v * 8);
+            }
+        }
+    };
+    load(row);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int v = threadIdx.x + k * lanes;
+        float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+        if (v < nvec) {
+            lo = __ldg(reinterpret_cast<const float4*>(a.weight) + 2 * v);
+            hi = __ldg(reinterpret_cast<const float4*>(a.weight) + 2 * v + 1);
+        }
+        w[k][0] = lo.x; w[k][1] = lo.y; w[k][2] = lo.z; w[k][3] = lo.w;
+        w[k][4] = hi.x; w[k][5] = hi.y; w[k][6] = hi.z; w[k][7] = hi.w;
+    }
+    // rows of a CTA leave the loop together, so its barriers stay aligned
+    for (int it = 0; row - threadIdx.y < a.M; row += stride, ++it) {
+        uint32_t h[NV][4];
+        float ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const uint32_t xw[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            const uint32_t rw[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[k][j] = kRes ? pack_bf16x2(bf16lo(xw[j]) + bf16lo(rw[j]), bf16hi(xw[j]) + bf16hi(rw[j])) : xw[j];
+                ss = fmaf(bf16lo(h[k][j]), bf16lo(h[k][j]), ss);
+                ss = fmaf(bf16hi(h[k][j]), bf16hi(h[k][j]), ss);
+            }
+        }
+        const bool live = row < a.M;
+        if (a.H != nullptr && live) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int v = threadIdx.x + k * lanes;
+                if (v < nvec)
+                    __stcs(reinterpret_cast<uint4*>(a.H + row * a.D + v * 8),
+                           make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]));
+            }
+        }
+        load(row + stride);
+        const float rstd = __frsqrt_rn(fmaf(row_sum(ss, red[it & 1], nwarps), inv_d, a.eps));
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int v = threadIdx.x + k * lanes;
+            uint32_t y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                y[j] = pack_bf16x2(bf16lo(h[k][j]) * rstd * w[k][2 * j], bf16hi(h[k][j]) * rstd * w[k][2 * j + 1]);
+            const uint4 yv = make_uint4(y[0], y[1], y[2], y[3]);
+            const bool mine = live && v < nvec;
+            if (a.Y != nullptr && mine) __stcs(reinterpret_cast<uint4*>(a.Y + row * a.D + v * 8), yv);
+            if (kCode >= 0) {
+                // D is a multiple of 64: a block's 8 lanes are all inside or all outside the row
+                float s;
+                const uint2 c = act8_encode<kCode < 0 ? 0 : kCode>(yv, act8_absmax(yv), &s);
+                if (mine) {
+                    const int64_t i = row * nvec + v;
+                    __stcs(reinterpret_cast<uint2*>(a.q.codes) + i, c);
+                    if ((v & 7) == 0) a.q.scales[i >> 3] = s;
+                }
+            }
+        }
+    }
+}
+
+template <int NV, bool kRes, bool kWeight>
+__global__ void __launch_bounds__(max_threads(NV))
+rmsnorm_backward_kernel(RmsNormGradArgs a) {
+    __shared__ float red[2][2][32];
+    const int nvec = a.D / 8, lanes = blockDim.x, nwarps = lanes / 32;
+    const int64_t stride = int64_t(gridDim.x) * blockDim.y;
+    int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    const float inv_d = 1.0f / static_cast<float>(a.D);
+    launch_dependents();                         // the sum of the partial dw waits for this grid
+
+    float w[NV][8], dw[NV][8];
+    uint4 g[NV], x[NV], r[NV];
+    auto load = [&](int64_t m) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int v = threadIdx.x + k * lanes;
+            g[k] = x[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (kRes) r[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (m < a.M && v < nvec) {
+                g[k] = ldg_stream(a.dY + m * a.D + v * 8);
+                x[k] = ldg_stream(a.H + m * a.D + v * 8);
+                if (kRes) r[k] = ldg_stream(a.dR + m * a.D + v * 8);
+            }
+        }
+    };
+    load(row);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int v = threadIdx.x + k * lanes;
+        float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+        if (v < nvec) {
+            lo = __ldg(reinterpret_cast<const float4*>(a.weight) + 2 * v);
+            hi = __ldg(reinterpret_cast<const float4*>(a.weight) + 2 * v + 1);
+        }
+        w[k][0] = lo.x; w[k][1] = lo.y; w[k][2] = lo.z; w[k][3] = lo.w;
+        w[k][4] = hi.x; w[k][5] = hi.y; w[k][6] = hi.z; w[k][7] = hi.w;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[k][j] = 0.f;
+    }
+    for (int it = 0; row - threadIdx.y < a.M; row += stride, ++it) {
+        uint4 gc[NV], xc[NV], rc[NV];
+        float ss = 0.f, st = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            gc[k] = g[k];
+            xc[k] = x[k];
+            if (kRes) rc[k] = r[k];
+            const uint32_t gw[4] = {g[k].x, g[k].y, g[k].z, g[k].w}, xw[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float h0 = bf16lo(xw[j]), h1 = bf16hi(xw[j]);
+                ss = fmaf(h0, h0, ss);
+                ss = fmaf(h1, h1, ss);
+                st = fmaf(bf16lo(gw[j]) * w[k][2 * j], h0, st);
+                st = fmaf(bf16hi(gw[j]) * w[k][2 * j + 1], h1, st);
+            }
+        }
+        load(row + stride);
+        ss = warp_sum(ss);
+        st = warp_sum(st);
+        if (nwarps > 1) {
+            float(*buf)[32] = red[it & 1];
+            if ((threadIdx.x & 31) == 0) {
+                buf[0][threadIdx.x >> 5] = ss;
+                buf[1][threadIdx.x >> 5] = st;
+            }
+            __syncthreads();
+            ss = st = 0.f;
+            for (int i = 0; i < nwarps; ++i) {
+                ss += buf[0][i];
+                st += buf[1][i];
+            }
+        }
+        const float rstd = __frsqrt_rn(fmaf(ss, inv_d, a.eps));
+        const float c = rstd * rstd * (st * inv_d);
+        const bool live = row < a.M;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int v = threadIdx.x + k * lanes;
+            const uint32_t gw[4] = {gc[k].x, gc[k].y, gc[k].z, gc[k].w}, xw[4] = {xc[k].x, xc[k].y, xc[k].z, xc[k].w};
+            const uint32_t rw[4] = {rc[k].x, rc[k].y, rc[k].z, rc[k].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float h0 = bf16lo(xw[j]), h1 = bf16hi(xw[j]), g0 = bf16lo(gw[j]), g1 = bf16hi(gw[j]);
+                float d0 = rstd * fmaf(-h0, c, g0 * w[k][2 * j]), d1 = rstd * fmaf(-h1, c, g1 * w[k][2 * j + 1]);
+                if (kRes) {
+                    d0 += bf16lo(rw[j]);
+                    d1 += bf16hi(rw[j]);
+                }
+                o[j] = pack_bf16x2(d0, d1);
+                if (kWeight && live) {
+                    dw[k][2 * j] = fmaf(g0, h0 * rstd, dw[k][2 * j]);
+                    dw[k][2 * j + 1] = fmaf(g1, h1 * rstd, dw[k][2 * j + 1]);
+                }
+            }
+            if (live && v < nvec)
+                __stcs(reinterpret_cast<uint4*>(a.dX + row * a.D + v * 8), make_uint4(o[0], o[1], o[2], o[3]));
+        }
+    }
+    if (!kWeight) return;
+    // one partial row of dw per CTA; the warps of a warp-per-row CTA add
+    // theirs in warp order through shared memory
+    extern __shared__ float sdw[];
+    if (blockDim.y > 1) {
+        if (threadIdx.y > 0) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int v = threadIdx.x + k * lanes;
+                if (v < nvec) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sdw[(threadIdx.y - 1) * a.D + v * 8 + j] = dw[k][j];
+                }
+            }
+        }
+        __syncthreads();
+        if (threadIdx.y > 0) return;
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int v = threadIdx.x + k * lanes;
+        if (v >= nvec) continue;
+        for (int q = 1; q < blockDim.y; ++q) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dw[k][j] += sdw[(q - 1) * a.D + v * 8 + j];
+        }
+        float4* p = reinterpret_cast<float4*>(a.part + int64_t(blockIdx.x) * a.D) + 2 * v;
+        p[0] = make_float4(dw[k][0], dw[k][1], dw[k][2], dw[k][3]);
+        p[1] = make_float4(dw[k][4], dw[k][5], dw[k][6], dw[k][7]);
+    }
+}
+
+// dw = (accumulate ? dw : 0) + the sum of the partial rows.  A CTA takes 32
+// columns; its 8 warps add interleaved rows and then, in warp order, one
+// another's sums: a fixed order.
+__global__ void __launch_bounds__(256)
+rmsnorm_dweight_kernel(const float* __restrict__ part, int parts, int D, float* dweight, int accumulate) {
+    __shared__ float s[8][32];
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+    float t = 0.f;
+    if (col < D)
+        for (int p = warp; p < parts; p += 8) t += part[int64_t(p) * D + col];
+    s[warp][lane] = t;
+    __syncthreads();
+    if (warp == 0 && col < D) {
+        for (int q = 1; q < 8; ++q) t += s[q][lane];
+        dweight[col] = accumulate ? dweight[col] + t : t;
+    }
+}
+
+struct Shape {
+    int nv;              // 16-byte words a lane holds of a row
+    dim3 block;          // lanes of a row x rows of a CTA
+    int64_t rows_ctas;   // CTAs if each took blockDim.y rows once
+};
+
+// A warp per row up to kWarpRowMax values.  Above it a CTA per row, with two
+// words a lane (bytes in flight per thread against threads per SM), four
+// where 512 lanes would not cover the row; with fewer rows than SMs one
+// word a lane, for the shortest path through a row.
+Shape shape_for(int64_t M, int D, int num_sms) {
+    const int nvec = D / 8;
+    Shape s;
+    if (D <= kWarpRowMax) {
+        s.nv = nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4;
+        const int64_t per = (M + num_sms - 1) / num_sms;
+        s.block = dim3(32, static_cast<unsigned>(per < kWarpRows ? (per < 1 ? 1 : per) : kWarpRows));
+    } else {
+        s.nv = nvec > 2 * max_threads(2) ? 4 : M <= num_sms && nvec <= max_threads(1) ? 1 : 2;
+        s.block = dim3(static_cast<unsigned>((nvec + s.nv * 32 - 1) / (s.nv * 32) * 32), 1);
+    }
+    s.rows_ctas = (M + s.block.y - 1) / s.block.y;
+    return s;
+}
+
+// CTAs of the persistent grid: threads resident at the kernels' register use
+unsigned grid_for(const Shape& s, int num_sms, int threads_per_sm) {
+    const int per_sm = threads_per_sm / static_cast<int>(s.block.x * s.block.y);
+    const int64_t cap = int64_t(num_sms) * (per_sm < 1 ? 1 : per_sm);
+    return static_cast<unsigned>(s.rows_ctas < cap ? s.rows_ctas : cap);
+}
+
+constexpr int kForwardThreads = 768;    // per SM
+constexpr int kBackwardThreads = 512;
+
+template <int NV, bool kRes>
+void run_forward(const RmsNormArgs& a, const Shape& s, unsigned grid, cudaStream_t st) {
+    if (a.q.codes == nullptr)
+        rmsnorm_forward_kernel<NV, kRes, -1><<<grid, s.block, 0, st>>>(a);
+    else if (a.q.code == QLORA_ACT8_E4M3)
+        rmsnorm_forward_kernel<NV, kRes, QLORA_ACT8_E4M3><<<grid, s.block, 0, st>>>(a);
+    else
+        rmsnorm_forward_kernel<NV, kRes, QLORA_ACT8_INT8><<<grid, s.block, 0, st>>>(a);
+}
+
+template <int NV>
+void run_forward(const RmsNormArgs& a, const Shape& s, unsigned grid, cudaStream_t st) {
+    if (a.R != nullptr) run_forward<NV, true>(a, s, grid, st);
+    else run_forward<NV, false>(a, s, grid, st);
+}
+
+template <int NV, bool kRes>
+void run_backward(const RmsNormGradArgs& a, const Shape& s, unsigned grid, cudaStream_t st) {
+    const size_t smem = a.dweight && s.block.y > 1 ? size_t(s.block.y - 1) * a.D * 4 : 0;
+    if (a.dweight) rmsnorm_backward_kernel<NV, kRes, true><<<grid, s.block, smem, st>>>(a);
+    else rmsnorm_backward_kernel<NV, kRes, false><<<grid, s.block, 0, st>>>(a);
+}
+
+template <int NV>
+void run_backward(const RmsNormGradArgs& a, const Shape& s, unsigned grid, cudaStream_t st) {
+    if (a.dR != nullptr) run_backward<NV, true>(a, s, grid, st);
+    else run_backward<NV, false>(a, s, grid, st);
+}
+
+}  // namespace
+
+int rmsnorm_max_width() { return kMaxWidth; }
+
+int rmsnorm_parts(int64_t M, int D, int num_sms) {
+    return static_cast<int>(grid_for(shape_for(M, D, num_sms), num_sms, kBackwardThreads));
+}
+
+cudaError_t launch_rmsnorm_forward(const RmsNormArgs& a, int num_sms, cudaStream_t st) {
+    const Shape s = shape_for(a.M, a.D, num_sms);
+    const unsigned grid = grid_for(s, num_sms, kForwardThreads);
+    switch (s.nv) {
+        case 1: run_forward<1>(a, s, grid, st); break;
+        case 2: run_forward<2>(a, s, grid, st); break;
+        default: run_forward<4>(a, s, grid, st); break;
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_rmsnorm_backward(const RmsNormGradArgs& a, int num_sms, cudaStream_t st) {
+    const Shape s = shape_for(a.M, a.D, num_sms);
+    const unsigned grid = grid_for(s, num_sms, kBackwardThreads);
+    switch (s.nv) {
+        case 1: run_backward<1>(a, s, grid, st); break;
+        case 2: run_backward<2>(a, s, grid, st); break;
+        default: run_backward<4>(a, s, grid, st); break;
+    }
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || a.dweight == nullptr) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((a.D + 31) / 32));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, rmsnorm_dweight_kernel, static_cast<const float*>(a.part),
+                              static_cast<int>(grid), a.D, a.dweight, a.accumulate);
+}
+
+}  // namespace qnf4

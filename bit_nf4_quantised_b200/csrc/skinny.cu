@@ -15,9 +15,15 @@
 // accumulated) and/or the zero-padded bf16 copy the tensor-core kernels
 // consume.  No partial buffer in HBM, no separate reduction launch, and a
 // fixed summation order.
+// P may also be a blockwise 8-bit copy (act8.cuh): X kept in 8 bits for the
+// backward.  A stage's 64 x 64 tile of P then holds one block per row, so the
+// ring carries the codes and one scale per row (5.25 KiB for 9 KiB), and each
+// warp expands the 16 rows or columns it multiplies to the bf16 values x~ in
+// a tile of its own just before its ldmatrix: only a warp-level barrier, and
+// the products are those of the bf16 kernel on x~.
 #include <cooperative_groups.h>
 
-#include "kernels.cuh"
+#include "act8.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -41,10 +47,21 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <bool PK, bool QK, int JT16>
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0)
+                 : "memory");
+}
+
+// 8-bit P: a stage's codes, 64 rows of 64 bytes (pitch 80: a warp's 16-byte
+// reads down a column of rows meet no bank twice), then a scale per row
+constexpr int kPitch8 = 80;
+constexpr int kScale8 = TI * kPitch8;
+
+template <bool PK, bool QK, int JT16, bool P8>
 struct SkinnyTile {
     static constexpr int JP = JT16 * 16;
-    static constexpr int kPBytes = TI * kPitchK;                        // 9216
+    static constexpr int kTileP = TI * kPitchK;                         // 9216: a bf16 tile
+    static constexpr int kPBytes = P8 ? kScale8 + TI * 4 : kTileP;
     static constexpr int kQPitch = QK ? kPitchK : (JP * 2 + 16);
     static constexpr int kQBytes = QK ? JP * kPitchK : TC * kQPitch;
     static constexpr int kStage = kPBytes + kQBytes;
@@ -52,14 +69,38 @@ struct SkinnyTile {
     // is large (r > 64) so that the ring stays within 200 KiB
     static constexpr int kStages = (200 * 1024 / kStage) < 8 ? (200 * 1024 / kStage) : 8;
     static constexpr int kRedBytes = TI * JP * 4;                       // fp32 partial tile
-    static constexpr int kSmem = (kStages * kStage > kRedBytes) ? kStages * kStage : kRedBytes;
+    static constexpr int kRing = kStages * kStage + (P8 ? kTileP : 0);  // the expanded tile follows the ring
+    static constexpr int kSmem = kRing > kRedBytes ? kRing : kRedBytes;
     static_assert(kStages >= 3, "skinny ring depth");
 };
 
-template <bool PK, bool QK, int JT16>
+// Expand this warp's part of a stage's 8-bit tile (at raw) to bf16 (at tile,
+// pitch kPitchK): the 16 rows it multiplies (PK), or its 16 columns.
+template <bool PK, int kCode>
+__device__ __forceinline__ void expand_tile(uint32_t raw, uint32_t tile, int warp, int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int e = lane + 32 * h;                              // 64 pieces of 16 codes
+        const int row = PK ? warp * 16 + (e & 15) : e;
+        const int col = PK ? (e >> 4) * 16 : warp * 16;
+        uint32_t c0, c1, c2, c3;
+        float s;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(c0), "=r"(c1), "=r"(c2), "=r"(c3) : "r"(raw + row * kPitch8 + col) : "memory");
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(raw + kScale8 + row * 4) : "memory");
+        const uint4 lo = act8_decode8<kCode>(make_uint2(c0, c1), s), hi = act8_decode8<kCode>(make_uint2(c2, c3), s);
+        const uint32_t dst = tile + row * kPitchK + col * 2;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w)
+                     : "memory");
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 16), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                     : "memory");
+    }
+}
+
+template <bool PK, bool QK, int JT16, bool P8>
 __global__ void __launch_bounds__(kThreads)
 skinny_kernel(SkinnyArgs a) {
-    using Tl = SkinnyTile<PK, QK, JT16>;
+    using Tl = SkinnyTile<PK, QK, JT16, P8>;
     extern __shared__ __align__(16) uint8_t smem[];
     // a dependent tensor-core GEMM may start streaming its weight tiles now;
     // it waits for this grid only before it reads this kernel's output
@@ -79,19 +120,31 @@ skinny_kernel(SkinnyArgs a) {
         const int64_t c0 = c_beg + int64_t(chunk) * TC;
         const uint32_t sp = sbase + st * Tl::kStage;
         const uint32_t sq = sp + Tl::kPBytes;
+        if (P8) {
+            // rows and columns of P in 64-wide blocks: c0 and i0 are multiples of 64
 #pragma unroll
-        for (int q = tid; q < TI * 8; q += kThreads) {          // P tile: 64 x 64
-            const int row = q >> 3, ch = q & 7;
-            const uint16_t* src;
-            bool ok;
-            if (PK) {
-                ok = (i0 + row < a.I) && (c0 + ch * 8 < c_end);
-                src = a.P + (i0 + row) * a.ldp + c0 + ch * 8;
-            } else {
-                ok = (c0 + row < c_end) && (i0 + ch * 8 < a.I);
-                src = a.P + (c0 + row) * a.ldp + i0 + ch * 8;
+            for (int q = tid; q < TI * 4; q += kThreads) {
+                const int row = q >> 2, ch = q & 3;
+                const bool ok = PK ? (i0 + row < a.I) && (c0 < c_end) : (c0 + row < c_end) && (i0 < a.I);
+                const int64_t at = PK ? (i0 + row) * a.ldp + c0 : (c0 + row) * a.ldp + i0;
+                cp_async16(sp + row * kPitch8 + ch * 16, a.P8 + (ok ? at + ch * 16 : 0), ok);
+                if (ch == 0) cp_async4(sp + kScale8 + row * 4, a.Pscale + (ok ? at >> 6 : 0), ok);
             }
-            cp_async16(sp + row * kPitchK + ch * 16, ok ? src : a.P, ok);
+        } else {
+#pragma unroll
+            for (int q = tid; q < TI * 8; q += kThreads) {          // P tile: 64 x 64
+                const int row = q >> 3, ch = q & 7;
+                const uint16_t* src;
+                bool ok;
+                if (PK) {
+                    ok = (i0 + row < a.I) && (c0 + ch * 8 < c_end);
+                    src = a.P + (i0 + row) * a.ldp + c0 + ch * 8;
+                } else {
+                    ok = (c0 + row < c_end) && (i0 + ch * 8 < a.I);
+                    src = a.P + (c0 + row) * a.ldp + i0 + ch * 8;
+                }
+                cp_async16(sp + row * kPitchK + ch * 16, ok ? src : a.P, ok);
+            }
         }
         if (QK) {
             for (int q = tid; q < Tl::JP * 8; q += kThreads) {
@@ -135,8 +188,17 @@ skinny_kernel(SkinnyArgs a) {
         __syncthreads();
         if (chunk + kStages - 1 < nchunks) load_stage(chunk + kStages - 1, (chunk + kStages - 1) % kStages);
         cp_async_commit();
-        const uint32_t sp = sbase + st * Tl::kStage;
-        const uint32_t sq = sp + Tl::kPBytes;
+        const uint32_t stage = sbase + st * Tl::kStage;
+        const uint32_t sp = P8 ? sbase + kStages * Tl::kStage : stage;
+        const uint32_t sq = stage + Tl::kPBytes;
+        if (P8) {
+            __syncwarp();                        // the warp has read the previous chunk's tile
+            if (a.p_code == QLORA_ACT8_E4M3)
+                expand_tile<PK, QLORA_ACT8_E4M3>(stage, sp, warp, lane);
+            else
+                expand_tile<PK, QLORA_ACT8_INT8>(stage, sp, warp, lane);
+            __syncwarp();
+        }
         const int mi = lane >> 3, r8 = lane & 7;
 #pragma unroll
         for (int kk = 0; kk < TC / 16; ++kk) {
@@ -252,10 +314,10 @@ skinny_kernel(SkinnyArgs a) {
     cluster.sync();            // keep every partial alive until the sum is done
 }
 
-template <bool PK, bool QK, int JT16>
+template <bool PK, bool QK, int JT16, bool P8>
 cudaError_t run_skinny(const SkinnyArgs& a, cudaStream_t stream) {
-    using Tl = SkinnyTile<PK, QK, JT16>;
-    cudaError_t e = cudaFuncSetAttribute(skinny_kernel<PK, QK, JT16>,
+    using Tl = SkinnyTile<PK, QK, JT16, P8>;
+    cudaError_t e = cudaFuncSetAttribute(skinny_kernel<PK, QK, JT16, P8>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Tl::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -272,20 +334,20 @@ cudaError_t run_skinny(const SkinnyArgs& a, cudaStream_t stream) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.programmatic ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, skinny_kernel<PK, QK, JT16>, a);
+    return cudaLaunchKernelEx(&cfg, skinny_kernel<PK, QK, JT16, P8>, a);
 }
 
-template <bool PK, bool QK>
+template <bool PK, bool QK, bool P8>
 cudaError_t dispatch_j(const SkinnyArgs& a, cudaStream_t stream) {
     switch ((a.J + 15) / 16) {
-        case 1: return run_skinny<PK, QK, 1>(a, stream);
-        case 2: return run_skinny<PK, QK, 2>(a, stream);
-        case 3: return run_skinny<PK, QK, 3>(a, stream);
-        case 4: return run_skinny<PK, QK, 4>(a, stream);
-        case 5: return run_skinny<PK, QK, 5>(a, stream);
-        case 6: return run_skinny<PK, QK, 6>(a, stream);
-        case 7: return run_skinny<PK, QK, 7>(a, stream);
-        case 8: return run_skinny<PK, QK, 8>(a, stream);
+        case 1: return run_skinny<PK, QK, 1, P8>(a, stream);
+        case 2: return run_skinny<PK, QK, 2, P8>(a, stream);
+        case 3: return run_skinny<PK, QK, 3, P8>(a, stream);
+        case 4: return run_skinny<PK, QK, 4, P8>(a, stream);
+        case 5: return run_skinny<PK, QK, 5, P8>(a, stream);
+        case 6: return run_skinny<PK, QK, 6, P8>(a, stream);
+        case 7: return run_skinny<PK, QK, 7, P8>(a, stream);
+        case 8: return run_skinny<PK, QK, 8, P8>(a, stream);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -295,10 +357,14 @@ cudaError_t dispatch_j(const SkinnyArgs& a, cudaStream_t stream) {
 cudaError_t launch_skinny(bool p_kmajor, bool q_kmajor, const SkinnyArgs& a, cudaStream_t stream) {
     if (a.I <= 0 || a.J <= 0 || a.splits < 1 || a.splits > kMaxSkinnySplits)
         return a.I <= 0 ? cudaSuccess : cudaErrorInvalidValue;
-    if (p_kmajor && q_kmajor) return dispatch_j<true, true>(a, stream);
-    if (p_kmajor && !q_kmajor) return dispatch_j<true, false>(a, stream);
-    if (!p_kmajor && !q_kmajor) return dispatch_j<false, false>(a, stream);
-    return dispatch_j<false, true>(a, stream);
+    if (a.P8 != nullptr) {           // the two products that read X: T = X A^T and dA^T = X^T (gamma U)
+        if (p_kmajor != q_kmajor) return cudaErrorInvalidValue;
+        return p_kmajor ? dispatch_j<true, true, true>(a, stream) : dispatch_j<false, false, true>(a, stream);
+    }
+    if (p_kmajor && q_kmajor) return dispatch_j<true, true, false>(a, stream);
+    if (p_kmajor && !q_kmajor) return dispatch_j<true, false, false>(a, stream);
+    if (!p_kmajor && !q_kmajor) return dispatch_j<false, false, false>(a, stream);
+    return dispatch_j<false, true, false>(a, stream);
 }
 
 }  // namespace qnf4

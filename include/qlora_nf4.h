@@ -537,6 +537,178 @@ QLORA_API int qlora_mlp_backward(const uint16_t* dY, const uint16_t* X, int64_t 
                                  size_t ws_bytes, qlora_stream_t stream);
 
 /*
+ * Activation checkpoints in 8 bits.  "QLoRA, explained", "Compute and memory
+ * cost": activation memory dominates at long sequence lengths, so gradient
+ * checkpointing is effectively mandatory, and its recomputed forward
+ * dequantises every block a third time per step.  Keeping an activation in
+ * blockwise 8 bits is the middle way: 1 1/16 bytes a value instead of 2, and
+ * nothing recomputed.  The pages print no format; this one follows their
+ * blockwise absmax scheme.
+ * A matrix [rows][cols] of bf16, cols % 64 == 0, in blocks of 64 consecutive
+ * values of a row, c the largest magnitude of the block:
+ *   scales : fp32, one per block, s = fp32(c / TOP)
+ *   codes  : one byte per value,
+ *            QLORA_ACT8_INT8 -- int8, TOP = 127, the integer nearest 127 x / c
+ *                               (ties to even);
+ *            QLORA_ACT8_E4M3 -- FP8 E4M3 (e4m3fn), TOP = 448, the code nearest
+ *                               448 x / c (ties to even).
+ *   read back as x~ = bf16_rne(fp32(code s)).
+ * The quotient is taken exactly; a zero of either sign has the code 0.  A
+ * block of zeros has s = 0; a block that holds a NaN or an infinity has
+ * s = NaN and reads back as NaN throughout.
+ * INT8 is off by at most c / 254 (before the rounding to bf16) and suits
+ * values of one size; E4M3 by at most 2^-4 of each value above 2^-6 c / 448,
+ * for blocks that a few outliers dominate.
+ */
+typedef enum {
+    QLORA_ACT8_INT8 = 0,
+    QLORA_ACT8_E4M3 = 1
+} qlora_act8_code;
+
+typedef struct {
+    void* codes;       /* device, rows * cols bytes, 16-byte aligned          */
+    float* scales;     /* device, rows * cols / 64 fp32, 16-byte aligned      */
+    int64_t rows;
+    int64_t cols;      /* a multiple of 64                                    */
+    int32_t code;      /* a qlora_act8_code                                   */
+} qlora_act8;
+
+/*
+ * qlora_act8_sizes -- byte sizes of the two buffers of a rows x cols copy.
+ * Host only.  Errors: QLORA_ERR_NULL, QLORA_ERR_SHAPE (a negative size, or
+ * rows * cols overflowing int64), QLORA_ERR_UNSUPPORTED (cols % 64 != 0).
+ */
+QLORA_API int qlora_act8_sizes(int64_t rows, int64_t cols, size_t* code_bytes, size_t* scale_bytes);
+
+/*
+ * qlora_act8_quantize -- the 8-bit copy of X (device, bf16, out->rows x
+ * out->cols, read); out (host struct) names the buffers, sizes and code.
+ * qlora_act8_dequantize -- x~ of every value (X_out: device, bf16, written).
+ * Zero rows or columns launch nothing; the pointers may then be NULL.
+ * Errors: QLORA_ERR_NULL, QLORA_ERR_SHAPE, QLORA_ERR_UNSUPPORTED (cols, or an
+ * unknown code), QLORA_ERR_ALIGN (every buffer 16-byte), QLORA_ERR_CUDA.
+ */
+QLORA_API int qlora_act8_quantize(const uint16_t* X, const qlora_act8* out, qlora_stream_t stream);
+QLORA_API int qlora_act8_dequantize(const qlora_act8* x, uint16_t* X_out, qlora_stream_t stream);
+
+/*
+ * qlora_swiglu_forward_act8 -- H = bf16(silu(G) * U) and, in the same pass,
+ * the 8-bit copies of G and U that the backward reads.
+ *   G, U (device, bf16, g8->rows x g8->cols, read); H (device, bf16, written;
+ *   may be G or U); g8, u8 (host structs of the same sizes and code, buffers
+ *   written).
+ * qlora_swiglu_backward_act8 -- from the copies, with g~, u~ their values,
+ *   dG = bf16(dH u~ silu'(g~)), dU = bf16(dH silu(g~)), H = bf16(silu(g~) u~).
+ *   dH (device, bf16, read); dG, dU (device, bf16, written; either may be
+ *   dH); H (device, bf16, nullable = not computed, written).
+ * Zero rows launch nothing.  Errors as qlora_act8_quantize, and
+ * QLORA_ERR_SHAPE if g8 and u8 differ in sizes or code.
+ */
+QLORA_API int qlora_swiglu_forward_act8(const uint16_t* G, const uint16_t* U, uint16_t* H,
+                                        const qlora_act8* g8, const qlora_act8* u8,
+                                        qlora_stream_t stream);
+QLORA_API int qlora_swiglu_backward_act8(const uint16_t* dH, const qlora_act8* g8,
+                                         const qlora_act8* u8, uint16_t* dG, uint16_t* dU,
+                                         uint16_t* H, qlora_stream_t stream);
+
+/*
+ * qlora_linear_backward_act8 -- qlora_linear_backward with the layer's input
+ * kept in 8 bits: x8 (host struct, M = x8->rows, cols = w->cols) in X's place.
+ * X enters only dA = scale (dY B)^T X, and X A^T when T_saved is NULL; both
+ * take x~ as it would read back, so every output equals, bit for bit, that
+ * of qlora_linear_backward on the dequantised input, which is never written.
+ * Pass T_saved from the forward to keep dB free of the 8-bit error.
+ * Errors: as qlora_linear_backward and qlora_act8_quantize, and
+ * QLORA_ERR_SHAPE if x8->cols is not w->cols.
+ */
+QLORA_API int qlora_linear_backward_act8(const uint16_t* dY, const qlora_act8* x8,
+                                         const qlora_nf4_tensor* w, const uint16_t* A,
+                                         const uint16_t* B, int r, float scale,
+                                         const float* T_saved, uint16_t* dX, float* dA, float* dB,
+                                         int accumulate, void* ws, size_t ws_bytes,
+                                         qlora_stream_t stream);
+
+/*
+ * The SwiGLU MLP with its activations kept in 8 bits instead of recomputed.
+ * qlora_mlp_forward_act8 -- Y as qlora_mlp_forward (the same bytes), and in
+ *   `saved` what the backward reads: the 8-bit copies g, u of gate(x) and
+ *   up(x) (M x F each, any code, the same for both) and the three layers'
+ *   X A^T (fp32, M x r, 16-byte aligned).  All of them are written.
+ * qlora_mlp_backward_act8 -- the gradients of qlora_mlp_backward from x8, an
+ *   8-bit copy of X (M x D; qlora_act8_quantize, or the copy that
+ *   qlora_rmsnorm_forward writes), and `saved`: no product with gate, up or
+ *   down is repeated, so each weight is dequantised once.  h is formed again
+ *   from g~ and u~ for dA_down.
+ * M = saved->g.rows.  ws as qlora_mlp_forward.  M = 0 as the calls above.
+ * Errors: those of qlora_mlp_forward / _backward and of
+ * qlora_linear_backward_act8; QLORA_ERR_SHAPE if a copy's size does not match.
+ */
+typedef struct {
+    qlora_act8 g, u;     /* M x F                                             */
+    float* T_gate;       /* device fp32 [M x r]                               */
+    float* T_up;
+    float* T_down;
+} qlora_mlp_saved8;
+
+QLORA_API int qlora_mlp_forward_act8(const uint16_t* X, const qlora_mlp* mlp, float scale,
+                                     uint16_t* Y, const qlora_mlp_saved8* saved, void* ws,
+                                     size_t ws_bytes, qlora_stream_t stream);
+QLORA_API int qlora_mlp_backward_act8(const uint16_t* dY, const qlora_act8* x8,
+                                      const qlora_mlp* mlp, float scale,
+                                      const qlora_mlp_saved8* saved, uint16_t* dX,
+                                      const qlora_mlp_grads* grads, int accumulate, void* ws,
+                                      size_t ws_bytes, qlora_stream_t stream);
+
+/*
+ * RMSNorm in front of an adapted layer, with the residual's addition.
+ *   h = bf16(x + r),   y = bf16(h rstd w),   rstd = 1 / sqrt(mean(h^2) + eps)
+ * over rows of D values, in fp32 from the bf16 inputs.  The weight is fp32
+ * ("Failure modes", "Silent fp32 casts": preparing a model for k-bit training
+ * casts its norms to fp32).
+ *
+ * qlora_rmsnorm_forward
+ *   X      (device, bf16, M x D, read)
+ *   R      (device, bf16, M x D, nullable, read): the residual stream; NULL:
+ *          h = x
+ *   weight (device, fp32, D, read)
+ *   H      (device, bf16, M x D, nullable, written): h, the new residual
+ *          stream and what the backward reads; may be X or R
+ *   Y      (device, bf16, M x D, nullable, written); may be X or R
+ *   y8     (host struct, nullable): an M x D 8-bit copy of y to write, equal
+ *          to qlora_act8_quantize of Y
+ * At least one of Y and y8 is given.  M = 0 launches nothing.
+ * Shape rules: D % 8 == 0 (D % 64 == 0 with y8), 8 <= D <= 16384.  A row with
+ * a NaN or an infinity gives what the formula gives in fp32; squares overflow
+ * for |h| above 2^63.
+ *
+ * qlora_rmsnorm_backward -- with t = w dy,
+ *   dx = bf16( rstd (t - h rstd^2 mean(h t)) + dr ),  the gradient of x and
+ *                                                     of r alike
+ *   dw = sum over rows of dy h rstd                   (fp32)
+ *   dY, H   (device, bf16, M x D, read)
+ *   dR      (device, bf16, M x D, nullable, read): the gradient that reaches
+ *           h past the norm
+ *   dX      (device, bf16, M x D, written; may be dY, H or dR)
+ *   dweight (device, fp32, D, nullable = frozen, written; accumulate != 0
+ *           adds to its contents); its sum is taken in a fixed order
+ *   ws      (device, >= qlora_rmsnorm_workspace_size bytes, 256-byte aligned;
+ *           only with dweight, else it may be NULL)
+ * M = 0 writes a zero dweight (or leaves it when accumulating).
+ *
+ * Errors: QLORA_ERR_NULL, QLORA_ERR_SHAPE (negative sizes, y8 not M x D),
+ * QLORA_ERR_UNSUPPORTED (D; eps negative or not finite; y8's code),
+ * QLORA_ERR_ALIGN (16-byte), QLORA_ERR_WORKSPACE, QLORA_ERR_CUDA.
+ */
+QLORA_API int qlora_rmsnorm_forward(const uint16_t* X, const uint16_t* R, const float* weight,
+                                    int64_t M, int64_t D, float eps, uint16_t* H, uint16_t* Y,
+                                    const qlora_act8* y8, qlora_stream_t stream);
+QLORA_API int qlora_rmsnorm_workspace_size(int64_t M, int64_t D, size_t* bytes);
+QLORA_API int qlora_rmsnorm_backward(const uint16_t* dY, const uint16_t* H, const uint16_t* dR,
+                                     const float* weight, int64_t M, int64_t D, float eps,
+                                     uint16_t* dX, float* dweight, int accumulate, void* ws,
+                                     size_t ws_bytes, qlora_stream_t stream);
+
+/*
  * qlora_set_gemm_wait_limit_us -- the bound, in microseconds, of every wait of
  * the tensor-core dequant-GEMM (the forward and dX kernel of
  * qlora_linear_forward / _backward) on its pipeline barriers, for GEMMs

@@ -718,3 +718,70 @@ def adamw8_step(p, g, m_state, v_state, t: int, lr: float, beta1: float, beta2: 
     p, m, v = adamw_step(p, g, m, v, t, lr, beta1, beta2, eps, weight_decay)
     return (p, encode_state8(m, True, block),
             encode_state8(np.sqrt(v).astype(np.float32), False, block))
+
+
+# ---------------------------------------------------------------------------
+# Activation checkpoints in 8 bits: blocks of 64 consecutive values of a row,
+# s = fp32(c / TOP) with c the block's largest magnitude, code = the int8 or
+# E4M3 code nearest TOP x / c (ties to even; the quotient exact: x is bf16, so
+# in fp64 TOP x is exact and the rounded quotient cannot cross a boundary of
+# the code), read back as bf16_rne(fp32(code s)).  A block with a non-finite
+# value has s = NaN and codes 0.
+# ---------------------------------------------------------------------------
+ACT8_TOP = {"int8": 127.0, "e4m3": 448.0}
+
+
+def act8_encode(x: np.ndarray, code: str):
+    """(codes, scales) of bf16-valued x with a multiple of 64 entries: codes
+    int8 or E4M3 bytes (uint8), scales fp32."""
+    b = np.asarray(x, np.float64).reshape(-1, BLOCK)
+    c = np.abs(b).max(axis=1)                       # NaN propagates
+    fine = np.isfinite(c)
+    top = ACT8_TOP[code]
+    scales = np.where(fine, np.where(fine, c, 0.0).astype(np.float32) / np.float32(top), np.float32("nan"))
+    live = fine & (c > 0)
+    q = np.where(live[:, None], np.where(live[:, None], b, 0.0) * top / np.where(live, c, 1.0)[:, None], 0.0)
+    if code == "int8":
+        codes = np.rint(q).astype(np.int8)
+    else:
+        mag = e4m3_encode_sorted(np.abs(q).astype(np.float32).reshape(-1)).reshape(q.shape)
+        codes = np.where(q < 0, 0x80, 0).astype(np.uint8) | mag      # a zero of either sign: code 0
+    return codes.reshape(-1), scales.astype(np.float32)
+
+
+def act8_decode_bits(codes: np.ndarray, scales: np.ndarray, code: str) -> np.ndarray:
+    """bf16 bits of the values an 8-bit copy reads back as."""
+    codes = np.asarray(codes).reshape(-1)
+    if code == "int8":
+        v = codes.astype(np.float32)
+    else:
+        u = codes.view(np.uint8)
+        v = np.where(u & 0x80, -e4m3_decode(u & 0x7F), e4m3_decode(u & 0x7F)).astype(np.float32)
+    x = (v.reshape(-1, BLOCK) * np.asarray(scales, np.float32)[:, None]).astype(np.float32).reshape(-1)
+    return np.where(np.isnan(x), np.uint16(0x7FC0), bf16_bits(np.where(np.isnan(x), np.float32(0), x)))
+
+
+def act8_decode(codes, scales, code: str) -> np.ndarray:
+    return bf16_bits_to_float(act8_decode_bits(codes, scales, code))
+
+
+# ---------------------------------------------------------------------------
+# RMSNorm of rows, y = h w / sqrt(mean(h^2) + eps), and its gradients.
+# ---------------------------------------------------------------------------
+def rmsnorm(h, w, eps):
+    h = np.asarray(h, np.float64)
+    return h / np.sqrt((h * h).mean(axis=1, keepdims=True) + eps) * np.asarray(w, np.float64)
+
+
+def rmsnorm_backward(dy, h, w, eps, dres=None):
+    """-> (dh, dw); dres is the gradient that reaches h past the norm."""
+    dy, h, w = (np.asarray(a, np.float64) for a in (dy, h, w))
+    rstd = 1.0 / np.sqrt((h * h).mean(axis=1, keepdims=True) + eps)
+    t = dy * w
+    dh = rstd * (t - h * rstd ** 2 * (h * t).mean(axis=1, keepdims=True))
+    return (dh if dres is None else dh + np.asarray(dres, np.float64)), (dy * h * rstd).sum(axis=0)
+
+
+def swiglu_backward(dh, g, u):
+    """(dg, du) of h = silu(g) u."""
+    return dh * u * silu_grad(g), dh * silu(g)
