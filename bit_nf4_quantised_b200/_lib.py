@@ -67,6 +67,8 @@ EXPORTED = (
     "qlora_rmsnorm_forward",
     "qlora_rmsnorm_workspace_size",
     "qlora_rmsnorm_backward",
+    "qlora_linear_fmt_workspace_size",
+    "qlora_linear_fmt_forward",
 )
 
 QLORA_SCALES_FP32 = 0
@@ -220,6 +222,9 @@ def lib() -> ctypes.CDLL:
                                                  vp, cz, vp]
         L.qlora_mlp_forward_act8.argtypes = [vp, mp, f32, vp, s8, vp, cz, vp]
         L.qlora_mlp_backward_act8.argtypes = [vp, a8, mp, f32, s8, vp, gp, i32, vp, cz, vp]
+        L.qlora_linear_fmt_workspace_size.argtypes = [i64, i64, i64, i32, fp, sz]
+        L.qlora_linear_fmt_forward.argtypes = [vp, i64, vp, vp, vp, i64, i64, fp, vp, vp, i32, f32, vp,
+                                               vp, cz, vp]
         L.qlora_rmsnorm_forward.argtypes = [vp, vp, vp, i64, i64, f32, vp, vp, a8, vp]
         L.qlora_rmsnorm_workspace_size.argtypes = [i64, i64, sz]
         L.qlora_rmsnorm_backward.argtypes = [vp, vp, vp, vp, i64, i64, f32, vp, vp, i32, vp, cz, vp]
@@ -988,3 +993,44 @@ def qlora_rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Tens
             None if dweight is None else ws.data_ptr(), 0 if dweight is None else ws.nbytes, _raw_stream()),
             "qlora_rmsnorm_backward")
     return dX, dweight
+
+
+def qlora_linear_fmt_workspace_size(M: int, N: int, K: int, r: int, fmt: Format) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().qlora_linear_fmt_workspace_size(M, N, K, r, fmt.c_struct(), ctypes.byref(b)),
+           "qlora_linear_fmt_workspace_size")
+    return b.value
+
+
+def qlora_linear_fmt_forward(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, meta, N: int,
+                             fmt: Format, A: torch.Tensor | None = None, B: torch.Tensor | None = None,
+                             scale: float = 0.0, Y: torch.Tensor | None = None,
+                             ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y = X W^T + scale * (X A^T) B^T for 1 to 16 tokens, W [N, K] stored in
+    fmt by qlora_quantize_fmt; without A and B, no adapter."""
+    M, K, dev = _matrix(X, "X")
+    r = 0 if A is None else A.shape[0]
+    if (A is None) != (B is None):
+        raise ValueError("A and B come together")
+    bf = torch.bfloat16
+    blocks = -(-N * K // fmt.block)
+    f32 = fmt.scales == QLORA_SCALES_FP32
+    with _on(X, stream):
+        Y = Y if Y is not None else torch.empty(M, N, dtype=bf, device=dev)
+        st = fmt.c_struct()
+        if ws is None:
+            b = ctypes.c_size_t()
+            _check(lib().qlora_linear_fmt_workspace_size(M, N, K, r, st, ctypes.byref(b)),
+                   "qlora_linear_fmt_workspace_size")
+            ws = torch.empty(b.value, dtype=torch.uint8, device=dev)
+        else:
+            _workspace(ws, 0, dev)
+        _check(lib().qlora_linear_fmt_forward(
+            X.data_ptr(), M, _arg(packed, torch.uint8, (blocks * fmt.block // 2,), dev, "packed"),
+            _arg(scales, torch.float32 if f32 else torch.uint8, (blocks,), dev, "scales"),
+            None if f32 else _arg(meta, torch.float32, (-(-blocks // GROUP),), dev, "meta"), N, K, st,
+            None if A is None else _arg(A, bf, (r, K), dev, "A"),
+            None if B is None else _arg(B, bf, (N, r), dev, "B"), r, float(scale),
+            _arg(Y, bf, (M, N), dev, "Y"), ws.data_ptr(), ws.nbytes, _raw_stream()),
+            "qlora_linear_fmt_forward")
+    return Y

@@ -224,7 +224,7 @@ cudaError_t launch_gemv(const CUtensorMap& tm_packed, const GemvArgs& a, int num
                         cudaStream_t stream);
 
 // T = sum of the t_parts partials (also to T_save);
-// Y = bf16(sum_s part[s] + gamma T B^T)
+// Y = bf16(sum_s part[s] + gamma T B^T), without T and B when r = 0
 struct GemvFinalizeArgs {
     const float* part;
     const float* Tpart;
@@ -238,6 +238,32 @@ struct GemvFinalizeArgs {
     int64_t M, N;
 };
 cudaError_t launch_gemv_finalize(const GemvFinalizeArgs& a, cudaStream_t stream);
+
+// ------------------------- products with a 4-bit weight in any stored format
+struct GemvFmtArgs {
+    const uint8_t* packed;
+    const void* scales;
+    const float* meta;
+    const uint16_t* X;         // [M x K] bf16, M <= 16
+    const uint16_t* A;         // [r x K] bf16
+    uint16_t* Y;               // [M x N] bf16, written when part is null
+    float* part;               // nullable: [splits][M][N] fp32 partial products
+    float* Tpart;              // [splits][t_ctas][M][r] fp32 partial X A^T (r > 0)
+    int64_t N, K;              // K % 64 == 0
+    int M, r;
+    int log2_block, scale_fmt;
+    uint16_t code[16];         // f16 bits of code * factor
+    float code_undo;           // 1 / factor
+    int chunks;                // 128-wide chunks per contraction slice (the rest by launch_gemv_fmt)
+    int warps_k;               // warps along the contraction, a power of two
+    int t_ctas;
+    int vec_scales;
+};
+struct GemvFmtPlan {
+    int splits, chunks, ctas, warps_k, rows, t_ctas;
+};
+GemvFmtPlan gemv_fmt_plan(int M, int64_t N, int64_t K, int r, int log2_block, int num_sms);
+cudaError_t launch_gemv_fmt(GemvFmtArgs a, const GemvFmtPlan& p, cudaStream_t s);
 
 // ----------------------------------------------- chained SwiGLU MLP (f3)
 // n = elements, a multiple of 8; H = bf16(silu(G) U); (G, U) <- (dG, dU);

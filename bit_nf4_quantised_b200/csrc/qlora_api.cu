@@ -2,6 +2,8 @@
 // Argument validation, the workspace plan, TMA descriptors, the NF4 codebook
 // construction, and the launch sequence of each entry point.  No device
 // memory is allocated here; every buffer is the caller's.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -1423,6 +1425,119 @@ int qlora_rmsnorm_backward(const uint16_t* dY, const uint16_t* H, const uint16_t
     a.D = static_cast<int>(D);
     a.eps = eps;
     return cuda_status(launch_rmsnorm_backward(a, sms, s));
+}
+
+}  // extern "C"
+
+// ------------------------- products with a 4-bit weight in any stored format
+namespace {
+
+// f16 codes of a codebook, times the factor (1, 3, 5, 7 or 15, and the power
+// of two that brings the largest code into [1, 2)) whose rounding errors,
+// relative to each code, are smallest; *undo = 1 / factor.  FP4 (multiples of
+// 1/12) and INT4 (of 1/7) become exact.
+void f16_codes(const qlora_format* f, uint16_t code[16], float* undo) {
+    double top = 0.0;
+    for (int i = 0; i < f->ncodes; ++i) top = std::max(top, std::fabs(double(f->codes[i])));
+    const double unit = std::ldexp(1.0, -std::ilogb(top));
+    double best = std::numeric_limits<double>::infinity();
+    for (const int k : {1, 3, 5, 7, 15}) {
+        uint16_t h[16] = {};
+        double err = 0.0;
+        for (int i = 0; i < f->ncodes; ++i) {
+            const double v = f->codes[i] * unit * k;
+            const __half x = __float2half_rn(static_cast<float>(v));
+            std::memcpy(&h[i], &x, 2);
+            const double d = v != 0.0 ? (double(__half2float(x)) - v) / v : 0.0;
+            err += d * d;
+        }
+        if (err < best * 0.999) {
+            best = err;
+            std::memcpy(code, h, sizeof(h));
+            *undo = static_cast<float>(1.0 / (unit * k));
+        }
+    }
+}
+
+int check_linear_fmt(int64_t M, int64_t N, int64_t K, int r, const qlora_format* f, FmtArgs* a) {
+    const int st = check_format(f, nullptr, a);
+    if (st != QLORA_OK) return st;
+    if (M < 0 || N < 0 || K < 0) return QLORA_ERR_SHAPE;
+    if (M > QLORA_GEMV_MAX_TOKENS || N < 1 || K < 64 || K % 64 != 0) return QLORA_ERR_UNSUPPORTED;
+    if (r < 0 || r > QLORA_MAX_RANK || r % 8 != 0) return QLORA_ERR_UNSUPPORTED;
+    if (N > (int64_t(1) << 31) - 1 || K > (int64_t(1) << 31) - 1) return QLORA_ERR_UNSUPPORTED;
+    return QLORA_OK;
+}
+
+// Workspace: the partial products and the partial T, where a second kernel
+// joins them; nothing when one kernel writes Y.
+int64_t linear_fmt_bytes(const GemvFmtPlan& p, int64_t M, int64_t N, int r, int64_t* off_t) {
+    if (p.splits == 1 && r == 0) return 0;
+    *off_t = up(int64_t(p.splits) * M * N * 4, kAlign);
+    return *off_t + up(int64_t(p.splits) * p.t_ctas * M * r * 4, kAlign);
+}
+
+}  // namespace
+
+extern "C" {
+
+int qlora_linear_fmt_workspace_size(int64_t M, int64_t N, int64_t K, int r, const qlora_format* f,
+                                    size_t* bytes) {
+    if (!bytes) return QLORA_ERR_NULL;
+    FmtArgs fa;
+    const int st = check_linear_fmt(M, N, K, r, f, &fa);
+    if (st != QLORA_OK) return st;
+    int64_t off = 0;
+    *bytes = M == 0 ? 0 : static_cast<size_t>(linear_fmt_bytes(
+        gemv_fmt_plan(static_cast<int>(M), N, K, r, fa.log2_block, num_sms()), M, N, r, &off));
+    return QLORA_OK;
+}
+
+int qlora_linear_fmt_forward(const uint16_t* X, int64_t M, const uint8_t* packed, const void* scales,
+                             const float* meta, int64_t N, int64_t K, const qlora_format* f,
+                             const uint16_t* A, const uint16_t* B, int r, float scale, uint16_t* Y,
+                             void* ws, size_t ws_bytes, qlora_stream_t stream) {
+    FmtArgs fa;
+    const int st = check_linear_fmt(M, N, K, r, f, &fa);
+    if (st != QLORA_OK) return st;
+    if (M == 0) return QLORA_OK;
+    if (!X || !Y || !packed || !scales || (fa.scale_fmt != QLORA_SCALES_FP32 && !meta)) return QLORA_ERR_NULL;
+    if (r > 0 && (!A || !B)) return QLORA_ERR_NULL;
+    // fp32 scales are read 16 bytes at a time
+    if (!aligned(X, 16) || !aligned(Y, 16) || !aligned(packed, 16) || !aligned(meta, 4) ||
+        !aligned(scales, fa.scale_fmt == QLORA_SCALES_FP32 ? 16 : 4) ||
+        (r > 0 && (!aligned(A, 16) || !aligned(B, 16))))
+        return QLORA_ERR_ALIGN;
+    const GemvFmtPlan p = gemv_fmt_plan(static_cast<int>(M), N, K, r, fa.log2_block, num_sms());
+    int64_t off_t = 0;
+    const int64_t need = linear_fmt_bytes(p, M, N, r, &off_t);
+    if (need > 0) {
+        if (!ws || ws_bytes < static_cast<size_t>(need)) return QLORA_ERR_WORKSPACE;
+        if (!aligned(ws, kAlign)) return QLORA_ERR_ALIGN;
+    }
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    GemvFmtArgs a{};
+    a.packed = packed;
+    a.scales = scales;
+    a.meta = meta;
+    a.X = X;
+    a.A = A;
+    a.Y = Y;
+    a.part = need > 0 ? at<float>(ws, 0) : nullptr;
+    a.Tpart = need > 0 ? at<float>(ws, off_t) : nullptr;
+    a.N = N;
+    a.K = K;
+    a.M = static_cast<int>(M);
+    a.r = r;
+    a.log2_block = fa.log2_block;
+    a.scale_fmt = fa.scale_fmt;
+    f16_codes(f, a.code, &a.code_undo);
+    QTRY(launch_gemv_fmt(a, p, s));
+    if (need > 0) {
+        GemvFinalizeArgs fin{a.part, a.Tpart, p.splits, p.splits * p.t_ctas, B, r, scale, nullptr, Y, M, N};
+        QTRY(launch_gemv_finalize(fin, s));
+    }
+    return QLORA_OK;
 }
 
 }  // extern "C"

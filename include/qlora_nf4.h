@@ -235,6 +235,37 @@ QLORA_API int qlora_dequantize_fmt(const uint8_t* packed, const void* scales, co
                                    qlora_stream_t stream);
 
 /*
+ * qlora_linear_fmt_forward -- decoding on a weight stored in any format f:
+ *   Y = X W^T + scale (X A^T) B^T   for 1 to 16 tokens,
+ * W[n][k] = codes[idx] c~_b, the stored weight of qlora_quantize_fmt for
+ * numel = N K (row-major, blocks along the flattened weight).
+ * One pass over the packed weight; W is not rounded to bf16 on the way.  Each
+ * code enters rounded to f16 after a common factor (FP4 and INT4 codes
+ * exactly, others within 2^-11 of themselves, or 2^-25 of the largest), the
+ * activations exactly down to 2^-28 of their token's largest value and the
+ * scales in fp32; sums are fp32, Y is rounded once.
+ *   X       (device, bf16, M x K, read), 0 <= M <= 16 (M = 0 launches nothing)
+ *   packed, scales, meta (device, read): as qlora_quantize_fmt writes them
+ *   A, B, r (device, bf16, r x K and N x r, read): the adapter, or r = 0 and
+ *           NULL for none; 0 <= r <= 128, r % 8 == 0
+ *   Y       (device, bf16, M x N, written)
+ *   ws      (device, >= qlora_linear_fmt_workspace_size bytes, 256-byte
+ *           aligned; may be NULL when that is 0)
+ * Shape rules: K % 64 == 0, K >= 64, N >= 1.  More tokens: expand the weight
+ * with qlora_dequantize_fmt and use a matrix product.
+ * Errors: QLORA_ERR_NULL, QLORA_ERR_SHAPE, QLORA_ERR_UNSUPPORTED (the format,
+ * M, N, K or r), QLORA_ERR_ALIGN (X, Y, A, B, packed and fp32 scales 16-byte;
+ * 8-bit scales and meta 4-byte), QLORA_ERR_WORKSPACE, QLORA_ERR_CUDA.
+ */
+QLORA_API int qlora_linear_fmt_workspace_size(int64_t M, int64_t N, int64_t K, int r,
+                                              const qlora_format* f, size_t* bytes);
+QLORA_API int qlora_linear_fmt_forward(const uint16_t* X, int64_t M, const uint8_t* packed,
+                                       const void* scales, const float* meta, int64_t N, int64_t K,
+                                       const qlora_format* f, const uint16_t* A, const uint16_t* B,
+                                       int r, float scale, uint16_t* Y, void* ws, size_t ws_bytes,
+                                       qlora_stream_t stream);
+
+/*
  * AdamW over an adapter matrix with 8-bit blockwise state ("QLoRA,
  * explained", "The algorithm, step by step": AdamW over A and B only, 32- or
  * 8-bit state; "Hyperparameters that matter": the 8-bit variant quantises
