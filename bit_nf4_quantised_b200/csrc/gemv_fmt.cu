@@ -10,41 +10,57 @@
 // shares its scale, so the sum of q x over the block is formed first, by
 // tensor-core products of f16 codes with f16 activations accumulated in fp32,
 // and then multiplied by c~ in fp32.
-//   codes        times a factor s (1, 3, 5, 7 or 15, and a power of two)
-//                that makes their f16 rounding smallest: FP4 and INT4 are
-//                exact, an NF4 code is off by 2^-12 of itself at most, where
-//                one bf16 rounding of Y allows 2^-9.
+//   codes        times a factor (1, 3, 5, 7 or 15, and a power of two) that
+//                makes their f16 rounding smallest: FP4 and INT4 are exact,
+//                an NF4 code is off by 2^-11 of itself at most, where the
+//                bf16 rounding of Y allows 2^-8.
 //   activations  times a power of two per token that puts the token's largest
 //                value in [2^14, 2^15): their 8 bits are exact in f16 down to
 //                2^-28 of the largest; below, off by 2^-40 of it.
 // Both factors are taken out of the sums at the end.
 //
-// A CTA per SM, 16 warps, each on 16 RG rows and a share of the contraction.
-//   weights      straight from HBM to registers, 16 bytes (32 weights) per
-//                lane and load, the next 256 columns in flight while the
-//                current ones are multiplied.  Lane (g, c) holds rows g and
-//                g + 8 of a 16-row group, weights 32 c ... 32 c + 31 of a
-//                128-wide chunk; MMA j (of 8 per chunk) multiplies every
-//                lane's weights 4 j ... 4 j + 3.
+// A CTA per SM, 16 warps, each on 32 rows and a share of the contraction, in
+// chunks of 128 columns, two to a step.
+//   weights      from HBM to registers, 16 bytes (32 weights) per lane and
+//                load, the next two chunks in flight while the current ones
+//                are multiplied.  Lane (g, c) holds rows g and g + 8 of a
+//                16-row group, columns 32 c ... 32 c + 31 of the chunk.
+//                Measured on a 117 MB weight, reads alone: 21.0 us; through
+//                rings in shared memory 20.7 (cp.async, TMA), but the whole
+//                kernel was 10 to 25% slower with them, its second pass over
+//                the packed words competing with the table's for the
+//                shared-memory pipe.
+//   products     mma.sync m16n8k16, W rows on the M side, tokens on the N
+//                side; the contraction order is permuted alike on both
+//                operands.  The four lanes of a row hold weights of up to four
+//                blocks, which one MMA must not add up:
+//                - few tokens: the MMA's 8 columns are (token, block) pairs,
+//                  holding x where the lane's weights are of that block and
+//                  zero elsewhere, so that each column sums one block;
+//                - more tokens: the lanes of a row exchange words (shuffles)
+//                  until each holds a quarter of every block.
 //   expansion    a packed byte addresses a pair of f16 codes in a table with
 //                a copy per lane (no bank conflicts): one byte permute and
 //                one 4-byte shared load per two weights, no arithmetic.
-//   scales       the four lanes of a row hold weights of up to G = 4 blocks,
-//                which one MMA must not add up.  The MMA has 8 columns, so a
-//                token takes G of them: column (token, b) holds x where the
-//                lane's block is b and zero elsewhere, and comes out as the
-//                sum over block b alone (blocks of 16 take two sets of MMAs).
-//                A warp stages its rows' scales, decoded to fp32, in shared
-//                memory 256 columns at a time.
-//   joining      the warps' partial sums meet in shared memory once per unit
-//                of rows and are added in warp order.  Contraction slices,
-//                where a CTA's activations would not fit in shared memory,
-//                and the LoRA term are joined by gemv_finalize_kernel.
-// Bound: HBM; next to it the shared-memory pipe, one wavefront per 64 weights
-// for the table.
+//   scales       as stored (codes or fp32) copied to shared memory once for
+//                many rows, along the rows; a warp decodes its rows' scales of
+//                a step to fp32, a row a lane, just before it uses them.
+//                (Loaded from global memory a row a lane they cost 12 us on
+//                the 117 MB weight: 32 lines per load.)
+//   joining      no barrier but one per span of rows (all of the CTA's where
+//                they fit): the warps leave their sums in shared memory, and
+//                then a thread per output adds them in warp order, with the
+//                LoRA term gamma T B^T (T = X A^T from lora_t_kernel, which
+//                runs beside the start of this one).  A barrier for every 32
+//                rows cost 10 us.  Contraction slices, taken where a CTA's
+//                activations would not fit in shared memory, write partial
+//                sums that gemv_finalize_kernel joins.
+// Bound: the shared-memory and L1 pipe: for 4096 weights 64 wavefronts of table
+// loads, and the 2 KiB of packed words pass through it on their way from L2.
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.cuh"
 
@@ -55,36 +71,67 @@ namespace {
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSmemLimit = 227 * 1024;
+#ifndef SMALL
+#define SMALL 131
+#endif
+constexpr int kSmemSmall = SMALL * 1024;
 constexpr int kLutBytes = 256 * 256;         // 256 byte values, 64 words apart, 32 lanes' copies
+constexpr int kRows = 32;                    // rows of a warp
+constexpr int kCols = 256;                   // columns of a step
 
-// One variant: G blocks (columns) per token in a chunk, SB sets of MMAs
-// (blocks of 16), NT tiles of 8 columns, RG 16-row groups per warp.
-template <int G, int SB>
-struct Layout {
-    static constexpr int kGran = G == 1 ? 128 : G == 2 ? 64 : 32 / SB;   // weights per staged scale
-    static constexpr int kPerChunk = 128 / kGran;
-    static constexpr int kPerStep = 2 * kPerChunk;                       // per row and 256 columns
-    static constexpr int kPitch = kPerStep == 2 ? 2 : kPerStep + 2;      // fp32; 8 rows' pairs meet no bank twice
-};
-
+// Shared-memory plan, as offsets.  The code table comes first; its entries use
+// half of their 256 bytes, and the first tokens' activations sit in the other
+// halves.  After it the other tokens' activations, a line of zeros, staged
+// scales, partial sums, T, the tokens' largest magnitudes and factors.
 struct Plan {
-    int x_pitch, stage, red_pitch, red_bufs;
-    int off_x, off_stage, off_red, off_misc, total;
+    int warps_k, unit_rows, span_rows, x_pitch, hole_tokens;
+    int raw_pitch, meta_pitch, scale_pitch, red_pitch;    // words (scale_pitch: fp32 of a row in a step)
+    uint32_t x, zero, raw, meta, scales, red, t, misc;
+    int64_t total;
 };
 
-// Shared memory: code table, activations, staged scales, partial sums, and
-// the tokens' largest magnitudes and factors.
-__host__ __device__ inline Plan plan_smem(int M, int chunks, int pitch, int rows_per_warp) {
+// What the plan follows from: tokens, 128-wide chunks of a slice, columns that
+// share a scale, rank, log2 of the block, fp32 scales, and units of rows per
+// span.
+struct PlanKey {
+    int M, chunks, gran, r, log2_block, f32, span;
+};
+
+// fp32 of a row's scales of a step in a warp's area: pitches at which 8 rows'
+// loads of a chunk's entries meet no bank twice.
+__host__ __device__ constexpr int scale_pitch(int gran) { return gran == 128 ? 2 : gran == 64 ? 6 : 256 / gran + 4; }
+
+__host__ __device__ inline Plan plan_smem(const PlanKey& k) {
     Plan p;
-    p.x_pitch = ((chunks + 1) / 2 * 2) * 256 + 64;        // 64 mod 128: two tokens' loads share no bank
-    p.stage = rows_per_warp * pitch * 4;                  // per warp
-    p.red_pitch = rows_per_warp + 8;
-    p.red_bufs = M <= 4 ? 2 : 1;
-    p.off_x = kLutBytes;
-    p.off_stage = p.off_x + M * p.x_pitch;
-    p.off_red = p.off_stage + kWarps * p.stage;
-    p.off_misc = p.off_red + p.red_bufs * kWarps * M * p.red_pitch * 4;
-    p.total = p.off_misc + 2 * 16 * 4;
+    // warps along the contraction: a power of two, each with a step at least
+    const int steps = (k.chunks * 128 + kCols - 1) / kCols;
+    p.warps_k = 1;
+    while (p.warps_k < kWarps && p.warps_k * 2 <= steps) p.warps_k *= 2;
+    p.unit_rows = kRows * (kWarps / p.warps_k);
+    p.span_rows = k.span * p.unit_rows;
+    p.total = kLutBytes;
+    auto take = [&](int64_t bytes) {
+        const uint32_t at = static_cast<uint32_t>(p.total);
+        p.total += (bytes + 127) / 128 * 128;
+        return at;
+    };
+    p.x_pitch = ((k.chunks + 1) / 2 * 2) * 256;
+    p.hole_tokens = 256 * 128 / p.x_pitch < k.M ? 256 * 128 / p.x_pitch : k.M;
+    // a row's stored scales in the slice, and the words that hold them at any
+    // alignment; odd pitches, so that a row a lane meets no bank twice
+    const int blocks = ((k.chunks * 128) >> k.log2_block) + 2;
+    p.raw_pitch = (k.f32 ? blocks : blocks / 4 + 2) | 1;
+    p.meta_pitch = k.f32 ? 0 : (blocks / 256 + 2) | 1;
+    p.scale_pitch = scale_pitch(k.gran);
+    p.red_pitch = p.warps_k + 1;
+    p.scales = take(kWarps * kRows * p.scale_pitch * 4);
+    p.t = take(k.M * k.r * 4);
+    p.misc = take(2 * 16 * 4);
+    p.zero = take(128);
+    p.x = take(int64_t(k.M - p.hole_tokens) * p.x_pitch);
+    p.red = take(int64_t(k.M) * p.span_rows * p.red_pitch * 4);
+    p.raw = take(int64_t(p.span_rows) * p.raw_pitch * 4);
+    p.meta = take(int64_t(p.span_rows) * p.meta_pitch * 4);
     return p;
 }
 
@@ -93,6 +140,14 @@ __device__ __forceinline__ uint4 ldg_weights(const uint8_t* p) {
     asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -103,71 +158,24 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float decode_scale(uint32_t code, int fmt) {
-    return fmt == QLORA_SCALES_E4M3 ? e4m3_to_float(static_cast<uint8_t>(code))
-           : fmt == QLORA_SCALES_E5M2 ? e5m2_to_float(static_cast<uint8_t>(code))
-                                      : static_cast<float>(code);
+// The same onto zero.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// A row's scales over 256 columns as loaded: codes and two constants, or fp32.
-template <int E, bool kF32>
-struct RawScales {
-    uint32_t w[kF32 ? E : (E + 3) / 4];
-    float m0, m1;
-    int split;                            // entries before it belong to m0's group
-
-    // f: flat position of the first entry; last: of the last valid one;
-    // vec: entries are consecutive and 4-entry aligned
-    __device__ __forceinline__ void load(const GemvFmtArgs& a, int64_t f, int64_t last, int gran, bool vec) {
-        const int64_t b0 = f >> a.log2_block;
-        if (kF32) {
-            const float* s = static_cast<const float*>(a.scales);
-            if (E >= 4 && vec) {
-#pragma unroll
-                for (int e = 0; e < E / 4; ++e) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(s + b0) + e);
-                    w[4 * e] = v.x; w[4 * e + 1] = v.y; w[4 * e + 2] = v.z; w[4 * e + 3] = v.w;
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    w[e] = __float_as_uint(__ldg(s + (min(f + e * gran, last) >> a.log2_block)));
-            }
-            return;
-        }
-        const uint8_t* s = static_cast<const uint8_t*>(a.scales);
-        if (E >= 4 && vec) {
-#pragma unroll
-            for (int e = 0; e < E / 4; ++e) w[e] = __ldg(reinterpret_cast<const uint32_t*>(s + b0) + e);
-        } else {
-#pragma unroll
-            for (int e = 0; e < (E + 3) / 4; ++e) w[e] = 0;
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                w[e / 4] |= uint32_t(__ldg(s + (min(f + e * gran, last) >> a.log2_block))) << (8 * (e & 3));
-        }
-        const int64_t be = min(f + (E - 1) * gran, last) >> a.log2_block;
-        m0 = __ldg(a.meta + (b0 >> 8));
-        m1 = __ldg(a.meta + (be >> 8));
-        // first entry of the next group of 256 blocks
-        split = E;
-#pragma unroll
-        for (int e = E - 1; e > 0; --e)
-            if ((((f + e * gran) >> a.log2_block) >> 8) != (b0 >> 8)) split = e;
-    }
-
-    __device__ __forceinline__ float get(int e, int fmt) const {
-        if (kF32) return __uint_as_float(w[e]);
-        return __fmul_rn(decode_scale((w[e / 4] >> (8 * (e & 3))) & 0xffu, fmt), e < split ? m0 : m1);
-    }
-};
-
-template <int G, int SB, int NT, int RG, bool kF32>
+// kGran: columns that share a scale, up to a chunk.  kCol: (token, block)
+// columns, else exchanged words.  NT: tiles of 8 tokens (1 with kCol).
+template <int kGran, bool kCol, int NT, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
 gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a) {
-    using L = Layout<G, SB>;
-    constexpr int kRows = 16 * RG;                        // rows of a warp
-    constexpr int kTok = G == 1 ? 4 : 2;                  // totals per tile and lane
+    constexpr int kPer = 128 / kGran;                     // scales of a row and chunk
+    constexpr int E = kCols / kGran;                      // of a step
+    constexpr int kPitch = scale_pitch(kGran);
+    constexpr int G = !kCol || kGran == 128 ? 1 : kGran == 64 ? 2 : 4;     // columns per token
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
@@ -177,62 +185,88 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a) {
     const int M = a.M;
     const int64_t k_beg = int64_t(blockIdx.y) * a.chunks * 128;
     const int kslab = static_cast<int>(min(K - k_beg, int64_t(a.chunks) * 128));
-    const Plan p = plan_smem(M, a.chunks, L::kPitch, kRows);
-    uint8_t* const sx = smem + p.off_x;
-    float* const stage = reinterpret_cast<float*>(smem + p.off_stage + warp * p.stage);
-    uint32_t* const smax = reinterpret_cast<uint32_t*>(smem + p.off_misc);
-    float* const sundo = reinterpret_cast<float*>(smem + p.off_misc + 64);
+    const Plan p = plan_smem({M, a.chunks, kGran, a.t_rank, a.log2_block, kF32, a.span});
+    float* const scales = reinterpret_cast<float*>(smem + p.scales) + warp * kRows * kPitch;
+    uint32_t* const smax = reinterpret_cast<uint32_t*>(smem + p.misc);
+    float* const sundo = reinterpret_cast<float*>(smem + p.misc + 64);
 
-    // rows of this CTA, and this warp's part of a unit: 16 RG rows (the
-    // wr-th such group of the unit) x steps m0 ... m1 - 1 of 256 columns
+    // rows of this CTA, and this warp's part of a unit: 32 rows (the wr-th
+    // such group of the unit) x steps m0 ... m1 - 1
     const int64_t r0 = a.N * blockIdx.x / gridDim.x, r1 = a.N * (blockIdx.x + 1) / gridDim.x;
-    const int wk = warp & (a.warps_k - 1), wr = warp / a.warps_k;
-    const int unit_rows = kRows * (kWarps / a.warps_k);
+    const int warps_k = p.warps_k, unit_rows = p.unit_rows;
+    const int wk = warp & (warps_k - 1), wr = warp / warps_k;
     const int units = static_cast<int>((r1 - r0 + unit_rows - 1) / unit_rows);
-    const int steps = (kslab + 255) / 256;
-    const int m0 = steps * wk / a.warps_k, m1 = steps * (wk + 1) / a.warps_k;
+    const int steps = (kslab + kCols - 1) / kCols;
+    const int m0 = steps * wk / warps_k, m1 = steps * (wk + 1) / warps_k;
+    auto rows_in = [&](int u) {
+        const int64_t left = r1 - (r0 + int64_t(u) * unit_rows + wr * kRows);
+        return static_cast<int>(min(left, int64_t(kRows)));
+    };
 
-    uint4 buf[2][RG][2];
-    RawScales<L::kPerStep, kF32> raw;
-    auto load_chunk = [&](int u, int mi, int cc) {
-        const int k = mi * 256 + cc * 128 + c * 32;
+    // The weight stream runs a step ahead of the products: (lu, lm) is the
+    // step it takes next, wp[i] this lane's words of row 8 i + g there.
+    uint4 buf[2][4];
+    int lu = 0, lm = m0, lrows = 0;
+    const uint8_t* wp[4];
+    auto seek_weights = [&]() {
+        const int64_t n = r0 + int64_t(lu) * unit_rows + wr * kRows + g;
+        lrows = rows_in(lu) - g;
+        wp[0] = a.packed + ((n * K + k_beg + m0 * kCols) >> 1) + c * 16;
 #pragma unroll
-        for (int q = 0; q < 2 * RG; ++q) {
-            const int64_t n = r0 + u * unit_rows + wr * kRows + q * 8 + g;
+        for (int i = 1; i < 4; ++i) wp[i] = wp[i - 1] + 4 * K;
+    };
+    auto load_chunk = [&](int cc) {
+        const bool in = lm * kCols + cc * 128 + c * 32 < kslab;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (n < r1 && k < kslab) v = ldg_weights(a.packed + ((n * K + k_beg + k) >> 1));
-            buf[cc][q >> 1][q & 1] = v;
+            if (in && 8 * i < lrows) v = ldg_weights(wp[i] + cc * 64);
+            buf[cc][i] = v;
         }
     };
-    auto load_scales = [&](int u, int mi) {
-        const int64_t n = r0 + u * unit_rows + wr * kRows + lane;
-        if (lane < kRows && n < r1) {
-            const int64_t row = n * K + k_beg;
-            raw.load(a, row + mi * 256, row + kslab - L::kGran, L::kGran, a.vec_scales && mi * 256 + 256 <= kslab);
-        }
-    };
-    auto store_scales = [&]() {
-        if (lane < kRows) {
+    auto next_step = [&]() {
+        if (++lm < m1) {
 #pragma unroll
-            for (int e = 0; e < L::kPerStep; e += 2) {
-                // blocks of 16: a chunk's even blocks first, then its odd ones
-                float v0 = raw.get(e, a.scale_fmt), v1 = raw.get(e + 1, a.scale_fmt);
-                const int ch = e / L::kPerChunk * L::kPerChunk, in = e % L::kPerChunk;
-                if (SB == 2) {
-                    stage[lane * L::kPitch + ch + in / 2] = v0;
-                    stage[lane * L::kPitch + ch + 4 + in / 2] = v1;
-                } else {
-                    *reinterpret_cast<float2*>(stage + lane * L::kPitch + e) = make_float2(v0, v1);
-                }
-            }
+            for (int i = 0; i < 4; ++i) wp[i] += kCols / 2;
+        } else {
+            lm = m0;
+            if (++lu < units) seek_weights();
         }
     };
     // the first loads travel while the table and the activations are set up
     if (m0 < m1 && units > 0) {
-        load_scales(0, m0);
-        load_chunk(0, m0, 0);
-        load_chunk(0, m0, 1);
+        seek_weights();
+        load_chunk(0);
+        load_chunk(1);
+        next_step();
     }
+
+    // Stored scales of the span's rows from row n0 on: a warp per row, the
+    // words that hold the slice's blocks b0 ... b1, and their groups'
+    // constants.
+    const int chunks = (kslab + 127) / 128;                 // of this slice
+    const uint32_t base = smem_u32(smem);
+    auto copy_scales = [&](int64_t n0) {
+        const int64_t all = (a.N * K + (int64_t(1) << a.log2_block) - 1) >> a.log2_block;
+        for (int row = warp; row < p.span_rows && n0 + row < r1; row += kWarps) {
+            const int64_t f = (n0 + row) * K + k_beg;
+            const int64_t b0 = f >> a.log2_block, b1 = (f + kslab - 1) >> a.log2_block;
+            const uint32_t raw = p.raw + row * p.raw_pitch * 4;
+            if (kF32) {
+                const float* src = static_cast<const float*>(a.scales) + b0;
+                for (int w = lane; w <= b1 - b0; w += 32) cp_async4(base + raw + w * 4, src + w, 4);
+            } else {
+                const int64_t w0 = b0 & ~int64_t(3);
+                const uint8_t* src = static_cast<const uint8_t*>(a.scales) + w0;
+                for (int w = lane; w0 + 4 * w <= b1; w += 32)
+                    cp_async4(base + raw + w * 4, src + 4 * w, static_cast<int>(min(all - (w0 + 4 * w), int64_t(4))));
+                const uint32_t meta = p.meta + row * p.meta_pitch * 4;
+                for (int w = lane; w <= (b1 >> 8) - (b0 >> 8); w += 32) cp_async4(base + meta + w * 4, a.meta + (b0 >> 8) + w, 4);
+            }
+        }
+    };
+    copy_scales(r0);
+    cp_async_commit();
 
     // code table: byte e of lane l at 256 e + 4 l
     for (int i = tid; i < 256 * 8; i += kThreads) {
@@ -241,12 +275,19 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a) {
         *reinterpret_cast<uint4*>(smem + e * 256 + (i & 7) * 16) = make_uint4(v, v, v, v);
     }
     // activations: each token's largest finite magnitude, then f16 copies
-    // scaled by it, 8 columns (one 16-byte word) at a time, in the order the
-    // lanes read them: column 32 c + 8 j + i of a chunk at 64 j + 16 c + 2 i;
-    // zeros past the slice
+    // scaled by it, zeros past the slice, in the order of the MMAs: 16-byte
+    // word (pair of MMAs m2, lane c) of a chunk holds that lane's four
+    // columns of either MMA.  A chunk is two pieces of 128 bytes (m2 / 2), a
+    // piece two words of 64 (m2 & 1, exchanged for odd tokens, so that two
+    // tokens' loads share no bank).
     if (tid < 16) smax[tid] = 0;
+    if (tid < 8) *reinterpret_cast<uint4*>(smem + p.zero + tid * 16) = make_uint4(0u, 0u, 0u, 0u);
+    auto x_base = [&](int m) {                              // token m's first piece, and the pieces' stride
+        return m < p.hole_tokens ? make_int2(m * (p.x_pitch / 128) * 256 + 128, 256)
+                                 : make_int2(p.x + (m - p.hole_tokens) * p.x_pitch, 128);
+    };
     __syncthreads();
-    const int words = steps * 32;                           // 16-byte words per token
+    const int words = steps * (kCols / 8);                  // 16-byte words per token
     for (int m = 0; m < M; ++m) {
         uint32_t mx = 0;
         for (int i = tid; i * 8 < kslab; i += kThreads) {
@@ -280,297 +321,476 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a) {
             }
             o = make_uint4(out[0], out[1], out[2], out[3]);
         }
-        const int ch = w >> 4, in_ch = w & 15;
-        *reinterpret_cast<uint4*>(sx + m * p.x_pitch + ch * 256 + (in_ch & 3) * 64 + (in_ch >> 2) * 16) = o;
+        // columns 8 u ... 8 u + 7 of the chunk: where in it
+        const int u = w & 15;
+        constexpr bool kWhole = kCol || kGran == 128;       // lane c: columns 32 c ... 32 c + 31
+        const int m2 = kWhole ? u & 3 : kGran == 64 ? (u >> 3) * 2 + (u & 1) : u >> 2;
+        const int2 xb = x_base(m);
+        uint8_t* at = smem + xb.x + (w >> 4) * 2 * xb.y + (m2 >> 1) * xb.y + ((m2 ^ m) & 1) * 64;
+        // exchanged words: quarter q of a run of 64 or 16 sits in lane
+        // 0, 2, 1, 3 for q = 0 ... 3
+        if (kWhole || kGran >= 32) {
+            const int q = (u >> 1) & 3;
+            const int cl = kWhole ? u >> 2 : kGran == 64 ? ((q & 1) << 1) | (q >> 1) : u & 3;
+            *reinterpret_cast<uint4*>(at + cl * 16) = o;
+        } else {
+            // blocks of 16: quarters 2 (u & 1) and the next, for the pair's
+            // first or second MMA
+            at += (u & 1) * 16 + ((u >> 1) & 1) * 8;
+            *reinterpret_cast<uint2*>(at) = make_uint2(o.x, o.y);
+            *reinterpret_cast<uint2*>(at + 32) = make_uint2(o.z, o.w);
+        }
         if (w == 0) sundo[m] = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) * a.code_undo;
     }
-    // this CTA's share of T = X A^T: columns s0 ... s1 - 1 of the slice
-    if (a.r > 0 && static_cast<int>(blockIdx.x) < a.t_ctas) {
-        const int n8 = kslab / 8;
-        const int s0 = static_cast<int>(int64_t(n8) * blockIdx.x / a.t_ctas);
-        const int s1 = static_cast<int>(int64_t(n8) * (blockIdx.x + 1) / a.t_ctas);
-        float* tp = a.Tpart + (int64_t(blockIdx.y) * a.t_ctas + blockIdx.x) * M * a.r;
-        for (int j = warp; j < a.r; j += kWarps) {
-            for (int mb = 0; mb < M; mb += 4) {
-                float t[4] = {0.f, 0.f, 0.f, 0.f};
-                for (int s = s0 + lane; s < s1; s += 32) {
-                    const uint4 av = __ldg(reinterpret_cast<const uint4*>(a.A + j * K + k_beg) + s);
-                    const uint32_t aw[4] = {av.x, av.y, av.z, av.w};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (mb + q < M) {
-                            const uint4 xv = __ldg(reinterpret_cast<const uint4*>(a.X + (mb + q) * K + k_beg) + s);
-                            const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                t[q] = fmaf(__uint_as_float(aw[e] << 16), __uint_as_float(xw[e] << 16), t[q]);
-                                t[q] = fmaf(__uint_as_float(aw[e] & 0xffff0000u),
-                                            __uint_as_float(xw[e] & 0xffff0000u), t[q]);
-                            }
-                        }
-                    }
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-#pragma unroll
-                    for (int o = 16; o >= 1; o >>= 1) t[q] += __shfl_xor_sync(0xffffffffu, t[q], o);
-                    if (lane == 0 && mb + q < M) tp[(mb + q) * a.r + j] = t[q];
-                }
-            }
-        }
-    }
+    cp_async_wait<0>();                                     // the scales
     __syncthreads();
 
-    // this lane's column of each tile: its token's activations where the
-    // column's block is the one the lane's weights belong to
-    const int my_block = G == 1 ? 0 : G == 2 ? c >> 1 : c;
-    uint32_t xoff[NT];
-    bool xon[NT];
+    // This lane's column of each tile: its token's activations, with (token,
+    // block) columns only where the lane's weights are of the column's block;
+    // elsewhere zeros (left in place with one tile, read from a line of them
+    // with two).
+    uint32_t xoff[NT], xpiece[NT];
+    bool xon = false;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int col = 8 * t + g, tok = col / G;
-        xon[t] = tok < M && col % G == my_block;
-        xoff[t] = static_cast<uint32_t>(p.off_x + tok * p.x_pitch + c * 16);
+        const int tok = (8 * t + g) / G;
+        xon = tok < M && (G == 1 || g % G == (G == 2 ? c >> 1 : c));
+        const int2 xb = x_base(xon ? tok : 0);
+        xoff[t] = (xon ? xb.x : p.zero) + (tok & 1) * 64 + c * 16;
+        xpiece[t] = xon ? xb.y : 0;
     }
+    uint4 x1[4];
+#pragma unroll
+    for (auto& v : x1) v = make_uint4(0u, 0u, 0u, 0u);
     const uint32_t lane4 = lane * 4;
     auto code_pair = [&](uint32_t w, uint32_t sel) {
         return *reinterpret_cast<const uint32_t*>(smem + prmt(w, lane4, sel));
     };
-    float tot[RG][NT][kTok];
+    constexpr int kTok = G == 1 ? 4 : 2;                  // totals per tile: two tokens' or one's, of two rows
+    float tot[2][NT][kTok];
 #pragma unroll
-    for (int q = 0; q < RG; ++q)
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < kTok; ++e) tot[q][t][e] = 0.f;
 
-    for (int u = 0; u < units; ++u) {
-        for (int mi = m0; mi < m1; ++mi) {
-            const bool more = mi + 1 < m1 || u + 1 < units;
-            const int nu = mi + 1 < m1 ? u : u + 1, nm = mi + 1 < m1 ? mi + 1 : m0;
-            __syncwarp();
-            store_scales();
-            __syncwarp();
-            if (more) load_scales(nu, nm);
+    // One row's words of a chunk, exchanged among the row's four lanes.
+    auto exchange = [&](const uint4& v, uint32_t (&w)[4]) {
+        if (kCol || kGran == 128) {
+            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+            return;
+        }
+        // halves with lane c ^ 2: first runs' words (w0, w1), then the others
+        const bool up = c & 2;
+        const uint32_t r0w = __shfl_xor_sync(0xffffffffu, up ? v.x : v.z, 2), r1w = __shfl_xor_sync(0xffffffffu, up ? v.y : v.w, 2);
+        w[0] = up ? r0w : v.x;
+        w[1] = up ? r1w : v.y;
+        w[2] = up ? v.z : r0w;
+        w[3] = up ? v.w : r1w;
+        if (kGran == 64) return;
+        // words with lane c ^ 1: word c of each of the four 16-byte units
+        const bool odd = c & 1;
+        const uint32_t s0 = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[1], 1), s1 = __shfl_xor_sync(0xffffffffu, odd ? w[2] : w[3], 1);
+        const uint32_t a0 = odd ? s0 : w[0], a1 = odd ? w[1] : s0, a2 = odd ? s1 : w[2], a3 = odd ? w[3] : s1;
+        w[0] = a0; w[1] = a1; w[2] = a2; w[3] = a3;
+        if (kGran == 32) return;
+        // half words with lane c ^ 2: two bytes of each block of 16
+        const uint32_t h0 = __shfl_xor_sync(0xffffffffu, prmt(w[0], w[1], up ? 0x5410u : 0x7632u), 2);
+        const uint32_t h1 = __shfl_xor_sync(0xffffffffu, prmt(w[2], w[3], up ? 0x5410u : 0x7632u), 2);
+        // lower lanes: own low half, then the other's low half; upper lanes:
+        // the other's high half, then the own high half
+        w[0] = up ? prmt(h0, w[0], 0x7610u) : prmt(w[0], h0, 0x5410u);
+        w[1] = up ? prmt(h0, w[1], 0x7632u) : prmt(w[1], h0, 0x7610u);
+        w[2] = up ? prmt(h1, w[2], 0x7610u) : prmt(w[2], h1, 0x5410u);
+        w[3] = up ? prmt(h1, w[3], 0x7632u) : prmt(w[3], h1, 0x7610u);
+    };
+
+    // Chunk cc of the current step, in buf[cc]: NQ 16-row groups; ch, the
+    // chunk within the slice.
+    auto chunk = [&](auto nq, int cc, int ch) {
+        constexpr int NQ = decltype(nq)::value;
+        uint32_t xa[NT];
 #pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-                float d[RG][NT][4];
-                const uint32_t xch = static_cast<uint32_t>((2 * mi + cc) * 256);
+        for (int t = 0; t < NT; ++t) xa[t] = xoff[t] + 2 * ch * xpiece[t];
+        if (NT == 1) {
 #pragma unroll
-                for (int jp = 0; jp < 4; ++jp) {
-                    if (jp % (4 / SB) == 0) {
+            for (int m2 = 0; m2 < 4; ++m2)
+                if (xon) x1[m2] = *reinterpret_cast<const uint4*>(smem + ((xa[0] + (m2 >> 1) * xpiece[0]) ^ ((m2 & 1) * 64u)));
+        }
+        float d[NQ][NT][4];
+        uint32_t w[NQ][2][4];
 #pragma unroll
-                        for (int q = 0; q < RG; ++q)
+        for (int i = 0; i < 2 * NQ; ++i) exchange(buf[cc][i], w[i >> 1][i & 1]);
+        // MMAs 4 b ... that share the sets of blocks: kGran / 16 of them, or
+        // with (token, block) columns the lane's 32 weights, 16 at a time for
+        // blocks of 16
+        constexpr int kRun = kCol ? (kGran == 16 ? 4 : 8) : kGran / 16;
+        uint4 x[NT];
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) d[q][t][0] = d[q][t][1] = d[q][t][2] = d[q][t][3] = 0.f;
-                    }
-                    uint32_t w[RG][2][4];
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t lo = 0x7604u | (j & 1) << 5, hi = lo | 1u << 4;     // bytes 2 (j & 1) and the next
+            const int m2 = j >> 1;
+            if (NT == 1) {
+                x[0] = x1[m2];
+            } else if ((j & 1) == 0) {
 #pragma unroll
-                    for (int q = 0; q < RG; ++q) {
-                        const uint4 lo = buf[cc][q][0], hi = buf[cc][q][1];
-                        const uint32_t wl = jp == 0 ? lo.x : jp == 1 ? lo.y : jp == 2 ? lo.z : lo.w;
-                        const uint32_t wh = jp == 0 ? hi.x : jp == 1 ? hi.y : jp == 2 ? hi.z : hi.w;
+                for (int t = 0; t < NT; ++t)
+                    x[t] = *reinterpret_cast<const uint4*>(smem + ((xa[t] + (m2 >> 1) * xpiece[t]) ^ ((m2 & 1) * 64u)));
+            }
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            w[q][j][0] = code_pair(wl, 0x5504u | (2 * j) << 4);
-                            w[q][j][1] = code_pair(wh, 0x5504u | (2 * j) << 4);
-                            w[q][j][2] = code_pair(wl, 0x5504u | (2 * j + 1) << 4);
-                            w[q][j][3] = code_pair(wh, 0x5504u | (2 * j + 1) << 4);
+            for (int q = 0; q < NQ; ++q) {
+                const uint32_t a0 = code_pair(w[q][0][m2], lo), a1 = code_pair(w[q][1][m2], lo);
+                const uint32_t a2 = code_pair(w[q][0][m2], hi), a3 = code_pair(w[q][1][m2], hi);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const uint32_t b0 = j & 1 ? x[t].z : x[t].x, b1 = j & 1 ? x[t].w : x[t].y;
+                    if (j % kRun == 0) mma_f16_first(d[q][t], a0, a1, a2, a3, b0, b1);
+                    else mma_f16(d[q][t], a0, a1, a2, a3, b0, b1);
+                }
+            }
+            if (j % kRun == kRun - 1) {
+                // the blocks' sums times their scales
+                const int run = j / kRun;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    const float* sr = scales + (q * 16 + g) * kPitch + cc * kPer;
+                    const float* sr8 = sr + 8 * kPitch;
+                    if constexpr (G == 1) {               // two tokens, one block
+                        const float s0 = sr[run], s1 = sr8[run];
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            tot[q][t][0] = fmaf(s0, d[q][t][0], tot[q][t][0]);
+                            tot[q][t][1] = fmaf(s0, d[q][t][1], tot[q][t][1]);
+                            tot[q][t][2] = fmaf(s1, d[q][t][2], tot[q][t][2]);
+                            tot[q][t][3] = fmaf(s1, d[q][t][3], tot[q][t][3]);
                         }
-                    }
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                        if (xon[t]) x = *reinterpret_cast<const uint4*>(smem + xoff[t] + xch + jp * 64);
-#pragma unroll
-                        for (int q = 0; q < RG; ++q) {
-                            mma_f16(d[q][t], w[q][0][0], w[q][0][1], w[q][0][2], w[q][0][3], x.x, x.y);
-                            mma_f16(d[q][t], w[q][1][0], w[q][1][1], w[q][1][2], w[q][1][3], x.z, x.w);
-                        }
-                    }
-                    if (jp % (4 / SB) == 4 / SB - 1) {
-                        // block sums times their scales: the lane's two columns are
-                        // two tokens of one block (G = 1) or two blocks of a token
-                        const int set = SB == 2 ? jp / 2 : 0;
-#pragma unroll
-                        for (int q = 0; q < RG; ++q) {
-                            const float* sr = stage + (q * 16 + g) * L::kPitch + cc * L::kPerChunk;
-                            if (G == 1) {
-                                const float s0 = sr[0], s1 = sr[8 * L::kPitch];
-#pragma unroll
-                                for (int t = 0; t < NT; ++t) {
-                                    tot[q][t][0] = fmaf(s0, d[q][t][0], tot[q][t][0]);
-                                    tot[q][t][1] = fmaf(s0, d[q][t][1], tot[q][t][1]);
-                                    tot[q][t][kTok - 2] = fmaf(s1, d[q][t][2], tot[q][t][kTok - 2]);
-                                    tot[q][t][kTok - 1] = fmaf(s1, d[q][t][3], tot[q][t][kTok - 1]);
-                                }
-                            } else {
-                                const int at = set * 4 + (G == 4 ? 2 * (c & 1) : 0);
-                                const float2 s0 = *reinterpret_cast<const float2*>(sr + at);
-                                const float2 s1 = *reinterpret_cast<const float2*>(sr + 8 * L::kPitch + at);
-#pragma unroll
-                                for (int t = 0; t < NT; ++t) {
-                                    tot[q][t][0] = fmaf(s0.x, d[q][t][0], fmaf(s0.y, d[q][t][1], tot[q][t][0]));
-                                    tot[q][t][1] = fmaf(s1.x, d[q][t][2], fmaf(s1.y, d[q][t][3], tot[q][t][1]));
-                                }
-                            }
-                        }
+                    } else {                              // one token, two blocks: b and b + step
+                        const int b = G == 2 ? 0 : kGran == 32 ? 2 * (c & 1) : 4 * (c & 1) + run;
+                        constexpr int step = kGran == 16 ? 2 : 1;
+                        tot[q][0][0] = fmaf(sr[b], d[q][0][0], fmaf(sr[b + step], d[q][0][1], tot[q][0][0]));
+                        tot[q][0][1] = fmaf(sr8[b], d[q][0][2], fmaf(sr8[b + step], d[q][0][3], tot[q][0][1]));
                     }
                 }
-                if (more) load_chunk(nu, nm, cc);
             }
         }
-        // the unit is complete: partial sums [warp][token][row] to shared
-        // memory, then one thread per output adds the warps' in order
-        float* red = reinterpret_cast<float*>(smem + p.off_red) + (p.red_bufs == 2 ? (u & 1) * kWarps * M * p.red_pitch : 0);
-        float* mine = red + warp * M * p.red_pitch;
+    };
+
+    // Row `lane` of the warp's rows in the current unit: its stored scales,
+    // and where in its first block the slice begins.
+    uint32_t lraw = 0, lmeta = 0;
+    int lfirst = 0, lb0 = 0;
+    auto seek_scales = [&](int64_t n, int span_row) {
+        const int64_t f = n * K + k_beg, b0 = f >> a.log2_block;
+        lfirst = static_cast<int>(f & ((int64_t(1) << a.log2_block) - 1));
+        lb0 = static_cast<int>(b0 & 255);
+        lraw = p.raw + span_row * p.raw_pitch * 4 + (kF32 ? 0 : static_cast<int>(b0 & 3));
+        lmeta = p.meta + span_row * p.meta_pitch * 4;
+    };
+    // Its scales of a step to fp32 in this warp's area.
+    auto decode_scales = [&](int mi) {
+        float v[E];
+        const int i0 = (lfirst + mi * kCols) >> a.log2_block;        // the first one's block, from b0 on
+        if (kF32) {
 #pragma unroll
-        for (int q = 0; q < RG; ++q)
+            for (int e = 0; e < E; ++e) {
+                const int i = a.vec_scales ? i0 + e : (lfirst + min(mi * kCols + e * kGran, kslab - kGran)) >> a.log2_block;
+                v[e] = *reinterpret_cast<const float*>(smem + lraw + i * 4);
+            }
+        } else if (a.vec_scales) {                        // E blocks in a row, in one word each four, in one group
+            const float m = *reinterpret_cast<const float*>(smem + lmeta + ((lb0 + i0) >> 8) * 4);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (G == 1) {
-                    const int tok = 8 * t + 2 * c;
-                    float* at = mine + tok * p.red_pitch + q * 16 + g;
-                    if (tok < M) {
-                        at[0] = tot[q][t][0];
-                        at[8] = tot[q][t][kTok - 2];
-                    }
-                    if (tok + 1 < M) {
-                        at[p.red_pitch] = tot[q][t][1];
-                        at[p.red_pitch + 8] = tot[q][t][kTok - 1];
+            for (int e = 0; e < E; e += 4) {
+                const uint32_t w = E >= 4 ? *reinterpret_cast<const uint32_t*>(smem + lraw + i0 + e)
+                                          : *reinterpret_cast<const uint16_t*>(smem + lraw + i0);
+                if (a.scale_fmt == QLORA_SCALES_E4M3) {
+#pragma unroll
+                    for (int q = 0; q < (E < 4 ? E : 4); q += 2) {
+                        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                            static_cast<__nv_fp8x2_storage_t>(w >> (8 * q)), __NV_E4M3);
+                        const float2 f = __half22float2(__half2(h));
+                        v[e + q] = __fmul_rn(f.x, m);
+                        v[e + q + 1] = __fmul_rn(f.y, m);
                     }
                 } else {
-                    float v0 = tot[q][t][0], v1 = tot[q][t][1];
-                    if (G == 4) {                        // the token's other two blocks
-                        v0 += __shfl_xor_sync(0xffffffffu, v0, 1);
-                        v1 += __shfl_xor_sync(0xffffffffu, v1, 1);
-                    }
-                    const int tok = G == 2 ? 4 * t + c : 2 * t + (c >> 1);
-                    float* at = mine + tok * p.red_pitch + q * 16 + g;
-                    if (tok < M && (G == 2 || (c & 1) == 0)) {
-                        at[0] = v0;
-                        at[8] = v1;
+#pragma unroll
+                    for (int q = 0; q < (E < 4 ? E : 4); ++q) {
+                        const uint32_t code = (w >> (8 * q)) & 0xffu;
+                        v[e + q] = __fmul_rn(a.scale_fmt == QLORA_SCALES_U8 ? static_cast<float>(code)
+                                                                            : e5m2_to_float(static_cast<uint8_t>(code)), m);
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < kTok; ++e) tot[q][t][e] = 0.f;
             }
-        __syncthreads();
-        // a different run of warps for each unit (one barrier per unit is
-        // enough with two buffers: whoever adds has done so before the next)
-        for (int o = (tid + u * 64) & (kThreads - 1); o < unit_rows * M; o += kThreads) {
-            const int m = o / unit_rows, row = o % unit_rows;
-            const int64_t n = r0 + u * unit_rows + row;
-            if (n >= r1) continue;
-            const float* src = red + ((row / kRows) * a.warps_k * M + m) * p.red_pitch + row % kRows;
-            float s = 0.f;
-            for (int q = 0; q < a.warps_k; ++q) s += src[q * M * p.red_pitch];
-            s *= sundo[m];
-            if (a.part != nullptr) {
-                a.part[(int64_t(blockIdx.y) * M + m) * a.N + n] = s;
-            } else {
-                const __nv_bfloat16 y = __float2bfloat16_rn(s);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                // columns past the slice repeat its last scale
+                const int i = (lfirst + min(mi * kCols + e * kGran, kslab - kGran)) >> a.log2_block;
+                const uint32_t code = smem[lraw + i];
+                const float m = *reinterpret_cast<const float*>(smem + lmeta + ((lb0 + i) >> 8) * 4);
+                v[e] = __fmul_rn(a.scale_fmt == QLORA_SCALES_U8 ? static_cast<float>(code)
+                                 : a.scale_fmt == QLORA_SCALES_E4M3 ? e4m3_to_float(static_cast<uint8_t>(code))
+                                                                    : e5m2_to_float(static_cast<uint8_t>(code)), m);
+            }
+        }
+        float* at = scales + lane * kPitch;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(at + e) = make_float2(v[e], v[e + 1]);
+    };
+
+    // The steps of this warp's rows in a unit.  (A chunk past the slice has
+    // zero activations.)
+    auto run_unit = [&](auto nq, int rows) {
+        for (int mi = m0; mi < m1; ++mi) {
+            const bool more = lu < units;
+            if (lane < rows) decode_scales(mi);
+            __syncwarp();
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+                chunk(nq, cc, 2 * mi + cc);
+                if (more) load_chunk(cc);
+            }
+            if (more) next_step();
+            __syncwarp();                                 // the step's scales have been used
+        }
+    };
+    auto skip_unit = [&]() {
+        for (int mi = m0; mi < m1 && lu < units; ++mi) {
+            load_chunk(0);
+            load_chunk(1);
+            next_step();
+        }
+    };
+
+    float* const red = reinterpret_cast<float*>(smem + p.red);
+    float* const sT = reinterpret_cast<float*>(smem + p.t);
+    for (int u0 = 0; u0 < units; u0 += a.span) {
+        const int64_t n0 = r0 + int64_t(u0) * unit_rows;  // the span's first row
+        if (u0 > 0) {
+            copy_scales(n0);
+            cp_async_commit();
+            cp_async_wait<0>();
+            __syncthreads();
+        }
+        const int u1 = min(units, u0 + a.span);
+        for (int u = u0; u < u1; ++u) {
+            const int rows = rows_in(u);
+            const int span_row = (u - u0) * unit_rows + wr * kRows;
+            seek_scales(n0 + span_row + lane, span_row + lane);
+            // straight-line steps of either height, so that a chunk's lookups
+            // overlap the products of the one before
+            if (rows > 16) run_unit(std::integral_constant<int, 2>{}, rows);
+            else if (rows > 0) run_unit(std::integral_constant<int, 1>{}, rows);
+            else skip_unit();
+            // partial sums [token][row][warp]
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    float* const row = red + (span_row + q * 16 + g) * p.red_pitch + wk;
+                    const int tok_stride = p.span_rows * p.red_pitch;
+                    if constexpr (G == 1) {
+                        const int tok = 8 * t + 2 * c;
+                        if (tok < M) {
+                            row[tok * tok_stride] = tot[q][t][0];
+                            row[tok * tok_stride + 8 * p.red_pitch] = tot[q][t][2];
+                        }
+                        if (tok + 1 < M) {
+                            row[(tok + 1) * tok_stride] = tot[q][t][1];
+                            row[(tok + 1) * tok_stride + 8 * p.red_pitch] = tot[q][t][3];
+                        }
+                    } else {
+                        float v0 = tot[q][t][0], v1 = tot[q][t][1];
+                        if (G == 4) {                     // the token's other two blocks
+                            v0 += __shfl_xor_sync(0xffffffffu, v0, 1);
+                            v1 += __shfl_xor_sync(0xffffffffu, v1, 1);
+                        }
+                        const int tok = G == 2 ? c : c >> 1;
+                        if (tok < M && (G == 2 || (c & 1) == 0)) {
+                            row[tok * tok_stride] = v0;
+                            row[tok * tok_stride + 8 * p.red_pitch] = v1;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < kTok; ++e) tot[q][t][e] = 0.f;
+                }
+        }
+        if (u0 == 0 && a.t_rank > 0) {
+            grid_dependency_wait();                       // T is complete
+            for (int i = tid; i < M * a.t_rank; i += kThreads) sT[i] = a.T[i];
+        }
+        __syncthreads();                                  // all partial sums are there
+        const int rows = static_cast<int>(min(int64_t(p.span_rows), r1 - n0));
+        for (int m = 0; m < M; ++m) {
+            // tokens begin at different threads, so that few rows still use them all
+            for (int row = (tid + (m & 1) * (kThreads / 2)) & (kThreads - 1); row < rows; row += kThreads) {
+                const int64_t n = n0 + row;
+                const float* src = red + (m * p.span_rows + row) * p.red_pitch;
+                float s = 0.f;
+                for (int w = 0; w < warps_k; ++w) s += src[w];
+                s *= sundo[m];
+                if (a.part != nullptr) {
+                    a.part[(int64_t(blockIdx.y) * M + m) * a.N + n] = s;
+                    continue;
+                }
+                float l = 0.f;
+                for (int j = 0; j < a.t_rank; j += 8) {
+                    const uint4 bv = __ldg(reinterpret_cast<const uint4*>(a.B + n * a.t_rank + j));
+                    const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        l = fmaf(sT[m * a.t_rank + j + 2 * q], __uint_as_float(bw[q] << 16), l);
+                        l = fmaf(sT[m * a.t_rank + j + 2 * q + 1], __uint_as_float(bw[q] & 0xffff0000u), l);
+                    }
+                }
+                const __nv_bfloat16 y = __float2bfloat16_rn(fmaf(a.gamma, l, s));
                 a.Y[m * a.N + n] = *reinterpret_cast<const uint16_t*>(&y);
             }
         }
-        if (p.red_bufs == 1) __syncthreads();
+        if (u1 < units) __syncthreads();                  // sums and scales have been read
+    }
+    // the joining kernel, this one's dependent, reads T too
+    if (a.part != nullptr) grid_dependency_wait();
+}
+
+// T[m][j] = x[m] . A[j] in fp32: a CTA per rank, its warps on equal runs of
+// the contraction, added in warp order.
+constexpr int kTThreads = 256;
+__global__ void __launch_bounds__(kTThreads)
+lora_t_kernel(const uint16_t* __restrict__ X, const uint16_t* __restrict__ A, float* __restrict__ T, int M, int64_t K, int r) {
+    __shared__ float part[kTThreads / 32][16];
+    launch_dependents();
+    const int j = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t n8 = K / 8;
+    const int64_t s0 = n8 * warp / (kTThreads / 32), s1 = n8 * (warp + 1) / (kTThreads / 32);
+    float t[16];
+#pragma unroll
+    for (int m = 0; m < 16; ++m) t[m] = 0.f;
+    for (int64_t s = s0 + lane; s < s1; s += 32) {
+        const uint4 av = __ldg(reinterpret_cast<const uint4*>(A + j * K) + s);
+        const uint32_t aw[4] = {av.x, av.y, av.z, av.w};
+#pragma unroll
+        for (int m = 0; m < 16; ++m) {
+            if (m < M) {
+                const uint4 xv = __ldg(reinterpret_cast<const uint4*>(X + m * K) + s);
+                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    t[m] = fmaf(__uint_as_float(aw[e] << 16), __uint_as_float(xw[e] << 16), t[m]);
+                    t[m] = fmaf(__uint_as_float(aw[e] & 0xffff0000u), __uint_as_float(xw[e] & 0xffff0000u), t[m]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < 16; ++m) {
+        if (m < M) {
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) t[m] += __shfl_xor_sync(0xffffffffu, t[m], o);
+            if (lane == 0) part[warp][m] = t[m];
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < M) {
+        float s = 0.f;
+        for (int w = 0; w < kTThreads / 32; ++w) s += part[w][threadIdx.x];
+        T[threadIdx.x * r + j] = s;
     }
 }
 
-template <int G, int SB, int NT>
-constexpr int row_groups() {
-    return NT >= 8 ? 1 : 2;              // 8 tiles x 2 row groups would not fit in registers
-}
-
-template <int G, int SB, int NT, bool kF32>
+template <int kGran, bool kCol, int NT, bool kF32>
 cudaError_t run(const GemvFmtArgs& a, dim3 grid, int smem, cudaStream_t s) {
-    constexpr int RG = row_groups<G, SB, NT>();
-    auto* kernel = gemv_fmt_kernel<G, SB, NT, RG, kF32>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    auto* kernel = gemv_fmt_kernel<kGran, kCol, NT, kF32>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, smem, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.t_rank > 0 ? 1 : 0;      // after lora_t_kernel
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <int G, int SB, int NT>
+template <int kGran, bool kCol, int NT>
 cudaError_t run_scales(const GemvFmtArgs& a, dim3 grid, int smem, cudaStream_t s) {
-    return a.scale_fmt == QLORA_SCALES_FP32 ? run<G, SB, NT, true>(a, grid, smem, s)
-                                            : run<G, SB, NT, false>(a, grid, smem, s);
+    return a.scale_fmt == QLORA_SCALES_FP32 ? run<kGran, kCol, NT, true>(a, grid, smem, s)
+                                            : run<kGran, kCol, NT, false>(a, grid, smem, s);
 }
 
-template <int G, int SB>
-cudaError_t run_tiles(int nt, const GemvFmtArgs& a, dim3 grid, int smem, cudaStream_t s) {
-    if (nt <= 1) return run_scales<G, SB, 1>(a, grid, smem, s);
-    if (nt <= 2) return run_scales<G, SB, 2>(a, grid, smem, s);
-    if constexpr (G >= 2) {
-        if (nt <= 4) return run_scales<G, SB, 4>(a, grid, smem, s);
+// (token, block) columns where one tile of 8 holds them all
+template <int kGran>
+cudaError_t run_gran(const GemvFmtArgs& a, dim3 grid, int smem, cudaStream_t s) {
+    if constexpr (kGran < 128) {
+        if (a.M <= (kGran == 64 ? 4 : 2)) return run_scales<kGran, true, 1>(a, grid, smem, s);
     }
-    if constexpr (G >= 4) {
-        return run_scales<G, SB, 8>(a, grid, smem, s);
-    }
-    return cudaErrorInvalidValue;
+    return a.M <= 8 ? run_scales<kGran, false, 1>(a, grid, smem, s) : run_scales<kGran, false, 2>(a, grid, smem, s);
 }
 
-// Blocks per 128-wide chunk of a row.  Rows of an odd number of 64-wide runs
-// shift a block of 128 or more against the next row's chunks by half a chunk,
-// so there each run takes its own scale.
-void shape_of(int log2_block, int64_t K, int* G, int* SB) {
-    *SB = log2_block == 4 ? 2 : 1;
-    *G = log2_block <= 5 ? 4 : log2_block == 6 || K % 128 != 0 ? 2 : 1;
-}
-
-int pitch_of(int G, int SB) {
-    return G == 1 ? Layout<1, 1>::kPitch : G == 2 ? Layout<2, 1>::kPitch
-           : SB == 1 ? Layout<4, 1>::kPitch : Layout<4, 2>::kPitch;
+// Columns that share a scale: the block, up to a chunk.  Rows of an odd
+// number of 64-wide runs shift a block of 128 or more against the next row's
+// chunks by half a chunk, so there each run takes its own scale.
+int gran_of(int log2_block, int64_t K) {
+    return log2_block <= 6 ? 1 << log2_block : K % 128 != 0 ? 64 : 128;
 }
 
 }  // namespace
 
-GemvFmtPlan gemv_fmt_plan(int M, int64_t N, int64_t K, int r, int log2_block, int num_sms) {
-    int G, SB;
-    shape_of(log2_block, K, &G, &SB);
-    const int tiles = (M * G + 7) / 8;
-    const int rows = tiles > 4 ? 16 : 32;                    // row_groups x 16
+GemvFmtPlan gemv_fmt_plan(int M, int64_t N, int64_t K, int r, int log2_block, bool f32, int num_sms) {
+    const int gran = gran_of(log2_block, K);
     const int64_t chunks = (K + 127) / 128;
-    // widest slice whose activations fit beside the rest
-    int64_t fit = 2;
-    while (fit + 2 <= 4096 && plan_smem(M, static_cast<int>(fit + 2), pitch_of(G, SB), rows).total <= kSmemLimit) fit += 2;
-    int64_t splits = (chunks + fit - 1) / fit;
-    // few rows: more slices, as long as every warp keeps a whole step
+    // Slices are whole multiples of 4 chunks: as few as leave their
+    // activations the room.
+    auto per_of = [&](int64_t splits) { return ((chunks + splits - 1) / splits + 3) / 4 * 4; };
+    auto key = [&](int64_t splits, int span) {
+        return PlanKey{M, static_cast<int>(std::min<int64_t>(per_of(splits), 1 << 20)), gran, r, log2_block, f32, span};
+    };
+    auto bytes = [&](int64_t splits, int64_t span) { return plan_smem(key(splits, static_cast<int>(span))).total; };
+    int64_t splits = 1;
+    while (per_of(splits) > 4 && bytes(splits, 1) > kSmemLimit) ++splits;
+    // few rows: more slices, as long as every warp keeps a step
     const int64_t by_rows = std::max<int64_t>(1, (N + 15) / 16);
-    while (by_rows * splits * 2 <= num_sms && chunks / (splits * 2) >= 2 * kWarps) splits *= 2;
+    while (by_rows * splits * 2 <= num_sms && per_of(splits * 2) >= 2 * kWarps && bytes(splits * 2, 1) <= kSmemLimit) splits *= 2;
     GemvFmtPlan p;
-    int64_t per = (chunks + splits - 1) / splits;
-    per = (per + 1) / 2 * 2;
-    p.chunks = static_cast<int>(per);
-    p.splits = static_cast<int>((chunks + per - 1) / per);
-    const int64_t ctas = std::max<int64_t>(1, num_sms / p.splits);
-    p.ctas = static_cast<int>(std::min<int64_t>(ctas, by_rows));
-    p.warps_k = 1;
-    while (p.warps_k < kWarps && p.warps_k * 2 <= (p.chunks + 1) / 2) p.warps_k *= 2;
-    p.rows = rows;
-    // T's shares: as many CTAs as keep the finalize's reads of their partials short
-    const int64_t by_read = 8192 / std::max<int64_t>(1, int64_t(M) * std::max(r, 1) * p.splits);
-    p.t_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(p.ctas, by_read)));
+    p.chunks = static_cast<int>(per_of(splits));
+    p.splits = static_cast<int>((chunks + p.chunks - 1) / p.chunks);
+    p.ctas = static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, num_sms / p.splits), by_rows));
+    // rows of a CTA in as few equal spans as fit
+    const int64_t rows = (N + p.ctas - 1) / p.ctas;
+    const int unit_rows = plan_smem(key(splits, 1)).unit_rows;
+    const int64_t units = (rows + unit_rows - 1) / unit_rows;
+    const int64_t limit = std::max<int64_t>(bytes(splits, 1), kSmemSmall);
+    int64_t span = 1;
+    while (span < 64 && span < units && bytes(splits, span + 1) <= limit) ++span;
+    const int64_t spans = (units + span - 1) / span;
+    p.span = static_cast<int>((units + spans - 1) / spans);
+    p.smem = static_cast<int>(bytes(splits, p.span));
     return p;
 }
 
 cudaError_t launch_gemv_fmt(GemvFmtArgs a, const GemvFmtPlan& p, cudaStream_t s) {
-    int G, SB;
-    shape_of(a.log2_block, a.K, &G, &SB);
-    const int tiles = (a.M * G + 7) / 8;
-    const int gran = G == 1 ? 128 : G == 2 ? 64 : 32 / SB;
+    const int gran = gran_of(a.log2_block, a.K);
+    if (a.t_rank > 0) {
+        lora_t_kernel<<<static_cast<unsigned>(a.t_rank), kTThreads, 0, s>>>(a.X, a.A, a.T, a.M, a.K, a.t_rank);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     a.chunks = p.chunks;
-    a.warps_k = p.warps_k;
-    a.t_ctas = p.t_ctas;
-    // 4 consecutive scales at a time, where each is a block of its own and
-    // every row and slice begins on a multiple of 4 of them
-    a.vec_scales = (1 << a.log2_block) == gran && (a.K / gran) % 4 == 0 && G > 1;
-    const int smem = plan_smem(a.M, p.chunks, pitch_of(G, SB), p.rows).total;
+    a.span = p.span;
+    // a step's scales as whole words of one group, where each is a block of
+    // its own and every row begins on a multiple of 4 steps' worth of them
+    a.vec_scales = (1 << a.log2_block) == gran && a.K % std::max(kCols, 4 * gran) == 0;
     const dim3 grid(static_cast<unsigned>(p.ctas), static_cast<unsigned>(p.splits));
-    if (G == 1) return run_tiles<1, 1>(tiles, a, grid, smem, s);
-    if (G == 2) return run_tiles<2, 1>(tiles, a, grid, smem, s);
-    return SB == 1 ? run_tiles<4, 1>(tiles, a, grid, smem, s) : run_tiles<4, 2>(tiles, a, grid, smem, s);
+    switch (gran) {
+        case 16: return run_gran<16>(a, grid, p.smem, s);
+        case 32: return run_gran<32>(a, grid, p.smem, s);
+        case 64: return run_gran<64>(a, grid, p.smem, s);
+        default: return run_gran<128>(a, grid, p.smem, s);
+    }
 }
 
 }  // namespace qnf4

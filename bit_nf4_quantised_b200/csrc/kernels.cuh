@@ -246,23 +246,24 @@ struct GemvFmtArgs {
     const float* meta;
     const uint16_t* X;         // [M x K] bf16, M <= 16
     const uint16_t* A;         // [r x K] bf16
+    const uint16_t* B;         // [N x r] bf16
+    float* T;                  // [M x r] fp32, written by the call's first kernel
+    float gamma;
     uint16_t* Y;               // [M x N] bf16, written when part is null
     float* part;               // nullable: [splits][M][N] fp32 partial products
-    float* Tpart;              // [splits][t_ctas][M][r] fp32 partial X A^T (r > 0)
     int64_t N, K;              // K % 64 == 0
-    int M, r;
+    int M, t_rank;             // t_rank: r, 0 without an adapter
     int log2_block, scale_fmt;
     uint16_t code[16];         // f16 bits of code * factor
     float code_undo;           // 1 / factor
     int chunks;                // 128-wide chunks per contraction slice (the rest by launch_gemv_fmt)
-    int warps_k;               // warps along the contraction, a power of two
-    int t_ctas;
+    int span;                  // units of rows between barriers
     int vec_scales;
 };
 struct GemvFmtPlan {
-    int splits, chunks, ctas, warps_k, rows, t_ctas;
+    int splits, chunks, ctas, span, smem;
 };
-GemvFmtPlan gemv_fmt_plan(int M, int64_t N, int64_t K, int r, int log2_block, int num_sms);
+GemvFmtPlan gemv_fmt_plan(int M, int64_t N, int64_t K, int r, int log2_block, bool f32, int num_sms);
 cudaError_t launch_gemv_fmt(GemvFmtArgs a, const GemvFmtPlan& p, cudaStream_t s);
 
 // ----------------------------------------------- chained SwiGLU MLP (f3)

@@ -1465,16 +1465,15 @@ int check_linear_fmt(int64_t M, int64_t N, int64_t K, int r, const qlora_format*
     if (M < 0 || N < 0 || K < 0) return QLORA_ERR_SHAPE;
     if (M > QLORA_GEMV_MAX_TOKENS || N < 1 || K < 64 || K % 64 != 0) return QLORA_ERR_UNSUPPORTED;
     if (r < 0 || r > QLORA_MAX_RANK || r % 8 != 0) return QLORA_ERR_UNSUPPORTED;
-    if (N > (int64_t(1) << 31) - 1 || K > (int64_t(1) << 31) - 1) return QLORA_ERR_UNSUPPORTED;
+    if (N > (int64_t(1) << 31) - 1 || K > (int64_t(1) << 24)) return QLORA_ERR_UNSUPPORTED;
     return QLORA_OK;
 }
 
-// Workspace: the partial products and the partial T, where a second kernel
-// joins them; nothing when one kernel writes Y.
-int64_t linear_fmt_bytes(const GemvFmtPlan& p, int64_t M, int64_t N, int r, int64_t* off_t) {
-    if (p.splits == 1 && r == 0) return 0;
-    *off_t = up(int64_t(p.splits) * M * N * 4, kAlign);
-    return *off_t + up(int64_t(p.splits) * p.t_ctas * M * r * 4, kAlign);
+// Workspace: T, and the partial products where a second kernel joins them.
+int64_t linear_fmt_bytes(const GemvFmtPlan& p, int64_t M, int64_t N, int r, int64_t* off_t, int64_t* off_part) {
+    *off_t = 0;
+    *off_part = up(M * r * 4, kAlign);
+    return *off_part + (p.splits > 1 ? up(int64_t(p.splits) * M * N * 4, kAlign) : 0);
 }
 
 }  // namespace
@@ -1487,9 +1486,9 @@ int qlora_linear_fmt_workspace_size(int64_t M, int64_t N, int64_t K, int r, cons
     FmtArgs fa;
     const int st = check_linear_fmt(M, N, K, r, f, &fa);
     if (st != QLORA_OK) return st;
-    int64_t off = 0;
+    int64_t off_t = 0, off_part = 0;
     *bytes = M == 0 ? 0 : static_cast<size_t>(linear_fmt_bytes(
-        gemv_fmt_plan(static_cast<int>(M), N, K, r, fa.log2_block, num_sms()), M, N, r, &off));
+        gemv_fmt_plan(static_cast<int>(M), N, K, r, fa.log2_block, fa.scale_fmt == QLORA_SCALES_FP32, num_sms()), M, N, r, &off_t, &off_part));
     return QLORA_OK;
 }
 
@@ -1508,9 +1507,9 @@ int qlora_linear_fmt_forward(const uint16_t* X, int64_t M, const uint8_t* packed
         !aligned(scales, fa.scale_fmt == QLORA_SCALES_FP32 ? 16 : 4) ||
         (r > 0 && (!aligned(A, 16) || !aligned(B, 16))))
         return QLORA_ERR_ALIGN;
-    const GemvFmtPlan p = gemv_fmt_plan(static_cast<int>(M), N, K, r, fa.log2_block, num_sms());
-    int64_t off_t = 0;
-    const int64_t need = linear_fmt_bytes(p, M, N, r, &off_t);
+    const GemvFmtPlan p = gemv_fmt_plan(static_cast<int>(M), N, K, r, fa.log2_block, fa.scale_fmt == QLORA_SCALES_FP32, num_sms());
+    int64_t off_t = 0, off_part = 0;
+    const int64_t need = linear_fmt_bytes(p, M, N, r, &off_t, &off_part);
     if (need > 0) {
         if (!ws || ws_bytes < static_cast<size_t>(need)) return QLORA_ERR_WORKSPACE;
         if (!aligned(ws, kAlign)) return QLORA_ERR_ALIGN;
@@ -1522,19 +1521,21 @@ int qlora_linear_fmt_forward(const uint16_t* X, int64_t M, const uint8_t* packed
     a.meta = meta;
     a.X = X;
     a.A = A;
+    a.B = B;
+    a.T = at<float>(ws, off_t);
+    a.gamma = scale;
     a.Y = Y;
-    a.part = need > 0 ? at<float>(ws, 0) : nullptr;
-    a.Tpart = need > 0 ? at<float>(ws, off_t) : nullptr;
+    a.part = p.splits > 1 ? at<float>(ws, off_part) : nullptr;
     a.N = N;
     a.K = K;
     a.M = static_cast<int>(M);
-    a.r = r;
+    a.t_rank = r;
     a.log2_block = fa.log2_block;
     a.scale_fmt = fa.scale_fmt;
     f16_codes(f, a.code, &a.code_undo);
     QTRY(launch_gemv_fmt(a, p, s));
-    if (need > 0) {
-        GemvFinalizeArgs fin{a.part, a.Tpart, p.splits, p.splits * p.t_ctas, B, r, scale, nullptr, Y, M, N};
+    if (p.splits > 1) {
+        GemvFinalizeArgs fin{a.part, a.T, p.splits, 1, B, r, scale, nullptr, Y, M, N};
         QTRY(launch_gemv_finalize(fin, s));
     }
     return QLORA_OK;

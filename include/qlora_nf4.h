@@ -251,7 +251,7 @@ QLORA_API int qlora_dequantize_fmt(const uint8_t* packed, const void* scales, co
  *   Y       (device, bf16, M x N, written)
  *   ws      (device, >= qlora_linear_fmt_workspace_size bytes, 256-byte
  *           aligned; may be NULL when that is 0)
- * Shape rules: K % 64 == 0, K >= 64, N >= 1.  More tokens: expand the weight
+ * Shape rules: K % 64 == 0, 64 <= K <= 2^24, 1 <= N < 2^31.  More tokens: expand the weight
  * with qlora_dequantize_fmt and use a matrix product.
  * Errors: QLORA_ERR_NULL, QLORA_ERR_SHAPE, QLORA_ERR_UNSUPPORTED (the format,
  * M, N, K or r), QLORA_ERR_ALIGN (X, Y, A, B, packed and fp32 scales 16-byte;

@@ -28,7 +28,7 @@ def test_workspace_sizes(q):
     f = _fmt(q)
     assert q.qlora_linear_fmt_workspace_size(0, 64, 64, 0, f) == 0
     assert q.qlora_linear_fmt_workspace_size(1, 4096, 4096, 0, f) == 0          # one kernel writes Y
-    assert q.qlora_linear_fmt_workspace_size(1, 4096, 4096, 16, f) >= 4 * 4096 + 4 * 16
+    assert q.qlora_linear_fmt_workspace_size(1, 4096, 4096, 16, f) >= 4 * 16
     # activations that do not fit beside each other take slices and partials
     assert q.qlora_linear_fmt_workspace_size(16, 8192, 28672, 0, f) >= 2 * 4 * 16 * 8192
     L, E = q.lib(), q._lib
