@@ -628,9 +628,7 @@ gemv_finalize_kernel(GemvFinalizeArgs a) {
     // in group order; with more values each thread sums whole columns.  The
     // order is fixed either way.
     const int E = static_cast<int>(a.M) * a.r;
-    if (E == 0) {
-        // no adapter: only the partial products are joined
-    } else if (E <= 256) {
+    if (E <= 256) {
         const int groups = 256 / E;
         const int e = threadIdx.x % E, gi = threadIdx.x / E;
         if (gi < groups) {

@@ -25,11 +25,13 @@
 //                load, the next two chunks in flight while the current ones
 //                are multiplied.  Lane (g, c) holds rows g and g + 8 of a
 //                16-row group, columns 32 c ... 32 c + 31 of the chunk.
-//                Measured on a 117 MB weight, reads alone: 21.0 us; through
-//                rings in shared memory 20.7 (cp.async, TMA), but the whole
-//                kernel was 10 to 25% slower with them, its second pass over
-//                the packed words competing with the table's for the
-//                shared-memory pipe.
+//                Reading a 117 MB weight this way and nothing else takes 21.0
+//                us; through rings in shared memory (cp.async, TMA) 20.7, but
+//                then the second pass over the packed words competes with the
+//                table's for the shared-memory pipe.
+//   shared memory  as little as the work allows, since what it leaves is L1,
+//                which the weight loads in flight need: 28672 x 8192 with one
+//                token took 47 us with 227 KiB reserved, 41 with 130.
 //   products     mma.sync m16n8k16, W rows on the M side, tokens on the N
 //                side; the contraction order is permuted alike on both
 //                operands.  The four lanes of a row hold weights of up to four
@@ -45,8 +47,7 @@
 //   scales       as stored (codes or fp32) copied to shared memory once for
 //                many rows, along the rows; a warp decodes its rows' scales of
 //                a step to fp32, a row a lane, just before it uses them.
-//                (Loaded from global memory a row a lane they cost 12 us on
-//                the 117 MB weight: 32 lines per load.)
+//                (Loaded from global memory a row a lane: 32 lines per load.)
 //   joining      no barrier but one per span of rows (all of the CTA's where
 //                they fit): the warps leave their sums in shared memory, and
 //                then a thread per output adds them in warp order, with the
@@ -54,9 +55,18 @@
 //                runs beside the start of this one).  A barrier for every 32
 //                rows cost 10 us.  Contraction slices, taken where a CTA's
 //                activations would not fit in shared memory, write partial
-//                sums that gemv_finalize_kernel joins.
+//                sums that join_slices_kernel adds.
 // Bound: the shared-memory and L1 pipe: for 4096 weights 64 wavefronts of table
-// loads, and the 2 KiB of packed words pass through it on their way from L2.
+// loads, and the 2 KiB of packed words pass through it on their way from L2
+// (lookups and products alone, on words already in registers: 81 cycles per
+// 4096 weights, 16.5 us for the 117 MB weight).
+// Measured (us; % of a 6568 GB/s copy on packed words and scales):
+//   28672 x 8192, NF4, blocks of 64, E4M3 scales: 40.0 with 1 token (46%),
+//   45.7 with 4, 71.7 with 8, 95.5 with 16; with rank 16, 1 token, 40.9
+//   28672 x 8192, NF4, blocks of 16, fp32 scales: 66.8 with 1 token, 149 with 16
+//   8192 x 28672, INT4, blocks of 128, fp32 scales: 42.1 with 1 token, 80.9 with 16
+//   11008 x 4096, NF4, blocks of 32, U8 scales, rank 64, 4 tokens: 21.8
+//   4096 x 4096, FP4, blocks of 16, E4M3 scales, 1 token: 8.0; NF4, blocks of 64: 7.4
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -71,10 +81,7 @@ namespace {
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSmemLimit = 227 * 1024;
-#ifndef SMALL
-#define SMALL 131
-#endif
-constexpr int kSmemSmall = SMALL * 1024;
+constexpr int kSmemSmall = 163 * 1024;       // leaves 92 KiB of L1: the weight loads in flight need it
 constexpr int kLutBytes = 256 * 256;         // 256 byte values, 64 words apart, 32 lanes' copies
 constexpr int kRows = 32;                    // rows of a warp
 constexpr int kCols = 256;                   // columns of a step
@@ -84,17 +91,17 @@ constexpr int kCols = 256;                   // columns of a step
 // halves.  After it the other tokens' activations, a line of zeros, staged
 // scales, partial sums, T, the tokens' largest magnitudes and factors.
 struct Plan {
-    int warps_k, unit_rows, span_rows, x_pitch, hole_tokens;
+    int unit_rows, span_rows, x_pitch, hole_tokens;
     int raw_pitch, meta_pitch, scale_pitch, red_pitch;    // words (scale_pitch: fp32 of a row in a step)
     uint32_t x, zero, raw, meta, scales, red, t, misc;
     int64_t total;
 };
 
 // What the plan follows from: tokens, 128-wide chunks of a slice, columns that
-// share a scale, rank, log2 of the block, fp32 scales, and units of rows per
-// span.
+// share a scale, rank, log2 of the block, fp32 scales, warps along the
+// contraction, and units of rows per span.
 struct PlanKey {
-    int M, chunks, gran, r, log2_block, f32, span;
+    int M, chunks, gran, r, log2_block, f32, warps_k, span;
 };
 
 // fp32 of a row's scales of a step in a warp's area: pitches at which 8 rows'
@@ -103,11 +110,7 @@ __host__ __device__ constexpr int scale_pitch(int gran) { return gran == 128 ? 2
 
 __host__ __device__ inline Plan plan_smem(const PlanKey& k) {
     Plan p;
-    // warps along the contraction: a power of two, each with a step at least
-    const int steps = (k.chunks * 128 + kCols - 1) / kCols;
-    p.warps_k = 1;
-    while (p.warps_k < kWarps && p.warps_k * 2 <= steps) p.warps_k *= 2;
-    p.unit_rows = kRows * (kWarps / p.warps_k);
+    p.unit_rows = kRows * (kWarps / k.warps_k);
     p.span_rows = k.span * p.unit_rows;
     p.total = kLutBytes;
     auto take = [&](int64_t bytes) {
@@ -123,7 +126,7 @@ __host__ __device__ inline Plan plan_smem(const PlanKey& k) {
     p.raw_pitch = (k.f32 ? blocks : blocks / 4 + 2) | 1;
     p.meta_pitch = k.f32 ? 0 : (blocks / 256 + 2) | 1;
     p.scale_pitch = scale_pitch(k.gran);
-    p.red_pitch = p.warps_k + 1;
+    p.red_pitch = k.warps_k + 1;
     p.scales = take(kWarps * kRows * p.scale_pitch * 4);
     p.t = take(k.M * k.r * 4);
     p.misc = take(2 * 16 * 4);
@@ -185,7 +188,7 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a) {
     const int M = a.M;
     const int64_t k_beg = int64_t(blockIdx.y) * a.chunks * 128;
     const int kslab = static_cast<int>(min(K - k_beg, int64_t(a.chunks) * 128));
-    const Plan p = plan_smem({M, a.chunks, kGran, a.t_rank, a.log2_block, kF32, a.span});
+    const Plan p = plan_smem({M, a.chunks, kGran, a.t_rank, a.log2_block, kF32, a.warps_k, a.span});
     float* const scales = reinterpret_cast<float*>(smem + p.scales) + warp * kRows * kPitch;
     uint32_t* const smax = reinterpret_cast<uint32_t*>(smem + p.misc);
     float* const sundo = reinterpret_cast<float*>(smem + p.misc + 64);
@@ -193,7 +196,7 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a) {
     // rows of this CTA, and this warp's part of a unit: 32 rows (the wr-th
     // such group of the unit) x steps m0 ... m1 - 1
     const int64_t r0 = a.N * blockIdx.x / gridDim.x, r1 = a.N * (blockIdx.x + 1) / gridDim.x;
-    const int warps_k = p.warps_k, unit_rows = p.unit_rows;
+    const int warps_k = a.warps_k, unit_rows = p.unit_rows;
     const int wk = warp & (warps_k - 1), wr = warp / warps_k;
     const int units = static_cast<int>((r1 - r0 + unit_rows - 1) / unit_rows);
     const int steps = (kslab + kCols - 1) / kCols;
@@ -244,7 +247,6 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a) {
     // Stored scales of the span's rows from row n0 on: a warp per row, the
     // words that hold the slice's blocks b0 ... b1, and their groups'
     // constants.
-    const int chunks = (kslab + 127) / 128;                 // of this slice
     const uint32_t base = smem_u32(smem);
     auto copy_scales = [&](int64_t n0) {
         const int64_t all = (a.N * K + (int64_t(1) << a.log2_block) - 1) >> a.log2_block;
@@ -288,39 +290,53 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a) {
     };
     __syncthreads();
     const int words = steps * (kCols / 8);                  // 16-byte words per token
-    for (int m = 0; m < M; ++m) {
-        uint32_t mx = 0;
-        for (int i = tid; i * 8 < kslab; i += kThreads) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.X + m * K + k_beg) + i);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint4* const xs = reinterpret_cast<const uint4*>(a.X + k_beg);
+    constexpr int kAhead = kCol ? 1 : 4;                               // words of a thread in flight
+    const int all_words = M * words;
+    uint4 xv[kAhead];
+    auto for_words = [&](bool fetch, auto use) {            // use(token, word, its value); the token is uniform in a
+        for (int base = tid; base < all_words; base += kAhead * kThreads) {        // warp: 32 | words
+            int m[kAhead], w[kAhead];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t lo = w[q] & 0x7fffu, hi = (w[q] >> 16) & 0x7fffu;
-                if (lo < 0x7f80u) mx = max(mx, lo);
-                if (hi < 0x7f80u) mx = max(mx, hi);
+            for (int i = 0; i < kAhead; ++i) {
+                const int at = base + i * kThreads;
+                m[i] = M == 1 ? 0 : at / words;
+                w[i] = at - m[i] * words;
+                if (fetch) {
+                    xv[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (at < all_words && w[i] * 8 < kslab) xv[i] = __ldg(xs + m[i] * (K / 8) + w[i]);
+                }
             }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (base + i * kThreads < all_words) use(m[i], w[i], xv[i]);
+        }
+    };
+    for_words(true, [&](int m, int, const uint4& v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t mx = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t lo = w[q] & 0x7fffu, hi = (w[q] >> 16) & 0x7fffu;
+            if (lo < 0x7f80u) mx = max(mx, lo);
+            if (hi < 0x7f80u) mx = max(mx, hi);
         }
         mx = __reduce_max_sync(0xffffffffu, mx);
         if (lane == 0) atomicMax(smax + m, mx);
-    }
+    });
     __syncthreads();
-    for (int i = tid; i < M * words; i += kThreads) {
-        const int m = i / words, w = i % words;
+    for_words(all_words > kAhead * kThreads, [&](int m, int w, const uint4& v) {
         const int sh = min(126, 14 + 127 - static_cast<int>(smax[m] >> 7));
         const float f = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-        uint4 o = make_uint4(0u, 0u, 0u, 0u);
-        if (w * 8 < kslab) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.X + m * K + k_beg) + w);
-            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-            uint32_t out[4];
+        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+        uint32_t out[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const __half2 h = __floats2half2_rn(__uint_as_float(in[q] << 16) * f,
-                                                    __uint_as_float(in[q] & 0xffff0000u) * f);
-                out[q] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            o = make_uint4(out[0], out[1], out[2], out[3]);
+        for (int q = 0; q < 4; ++q) {
+            const __half2 h = __floats2half2_rn(__uint_as_float(in[q] << 16) * f,
+                                                __uint_as_float(in[q] & 0xffff0000u) * f);
+            out[q] = *reinterpret_cast<const uint32_t*>(&h);
         }
+        const uint4 o = make_uint4(out[0], out[1], out[2], out[3]);
         // columns 8 u ... 8 u + 7 of the chunk: where in it
         const int u = w & 15;
         constexpr bool kWhole = kCol || kGran == 128;       // lane c: columns 32 c ... 32 c + 31
@@ -341,7 +357,7 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a) {
             *reinterpret_cast<uint2*>(at + 32) = make_uint2(o.z, o.w);
         }
         if (w == 0) sundo[m] = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) * a.code_undo;
-    }
+    });
     cp_async_wait<0>();                                     // the scales
     __syncthreads();
 
@@ -621,31 +637,30 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a) {
         }
         __syncthreads();                                  // all partial sums are there
         const int rows = static_cast<int>(min(int64_t(p.span_rows), r1 - n0));
-        for (int m = 0; m < M; ++m) {
-            // tokens begin at different threads, so that few rows still use them all
-            for (int row = (tid + (m & 1) * (kThreads / 2)) & (kThreads - 1); row < rows; row += kThreads) {
-                const int64_t n = n0 + row;
-                const float* src = red + (m * p.span_rows + row) * p.red_pitch;
-                float s = 0.f;
-                for (int w = 0; w < warps_k; ++w) s += src[w];
-                s *= sundo[m];
-                if (a.part != nullptr) {
-                    a.part[(int64_t(blockIdx.y) * M + m) * a.N + n] = s;
-                    continue;
-                }
-                float l = 0.f;
-                for (int j = 0; j < a.t_rank; j += 8) {
-                    const uint4 bv = __ldg(reinterpret_cast<const uint4*>(a.B + n * a.t_rank + j));
-                    const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        l = fmaf(sT[m * a.t_rank + j + 2 * q], __uint_as_float(bw[q] << 16), l);
-                        l = fmaf(sT[m * a.t_rank + j + 2 * q + 1], __uint_as_float(bw[q] & 0xffff0000u), l);
-                    }
-                }
-                const __nv_bfloat16 y = __float2bfloat16_rn(fmaf(a.gamma, l, s));
-                a.Y[m * a.N + n] = *reinterpret_cast<const uint16_t*>(&y);
+        for (int o = tid; o < M * rows; o += kThreads) {
+            const int m = M == 1 ? 0 : o / rows, row = o - m * rows;
+            const int64_t n = n0 + row;
+            const float* src = red + (m * p.span_rows + row) * p.red_pitch;
+            float s = 0.f;
+            for (int w = 0; w < warps_k; ++w) s += src[w];
+            s *= sundo[m];
+            if (a.part != nullptr) {
+                a.part[(int64_t(blockIdx.y) * M + m) * a.N + n] = s;
+                continue;
             }
+            float l = 0.f;
+#pragma unroll 2
+            for (int j = 0; j < a.t_rank; j += 8) {
+                const uint4 bv = __ldg(reinterpret_cast<const uint4*>(a.B + n * a.t_rank + j));
+                const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    l = fmaf(sT[m * a.t_rank + j + 2 * q], __uint_as_float(bw[q] << 16), l);
+                    l = fmaf(sT[m * a.t_rank + j + 2 * q + 1], __uint_as_float(bw[q] & 0xffff0000u), l);
+                }
+            }
+            const __nv_bfloat16 y = __float2bfloat16_rn(fmaf(a.gamma, l, s));
+            a.Y[m * a.N + n] = *reinterpret_cast<const uint16_t*>(&y);
         }
         if (u1 < units) __syncthreads();                  // sums and scales have been read
     }
@@ -655,7 +670,8 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a) {
 
 // T[m][j] = x[m] . A[j] in fp32: a CTA per rank, its warps on equal runs of
 // the contraction, added in warp order.
-constexpr int kTThreads = 256;
+constexpr int kTThreads = 512;
+template <int kM>
 __global__ void __launch_bounds__(kTThreads)
 lora_t_kernel(const uint16_t* __restrict__ X, const uint16_t* __restrict__ A, float* __restrict__ T, int M, int64_t K, int r) {
     __shared__ float part[kTThreads / 32][16];
@@ -663,14 +679,15 @@ lora_t_kernel(const uint16_t* __restrict__ X, const uint16_t* __restrict__ A, fl
     const int j = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t n8 = K / 8;
     const int64_t s0 = n8 * warp / (kTThreads / 32), s1 = n8 * (warp + 1) / (kTThreads / 32);
-    float t[16];
+    float t[kM];
 #pragma unroll
-    for (int m = 0; m < 16; ++m) t[m] = 0.f;
+    for (int m = 0; m < kM; ++m) t[m] = 0.f;
+#pragma unroll(kM == 1 ? 4 : kM == 4 ? 2 : 1)
     for (int64_t s = s0 + lane; s < s1; s += 32) {
         const uint4 av = __ldg(reinterpret_cast<const uint4*>(A + j * K) + s);
         const uint32_t aw[4] = {av.x, av.y, av.z, av.w};
 #pragma unroll
-        for (int m = 0; m < 16; ++m) {
+        for (int m = 0; m < kM; ++m) {
             if (m < M) {
                 const uint4 xv = __ldg(reinterpret_cast<const uint4*>(X + m * K) + s);
                 const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
@@ -683,7 +700,7 @@ lora_t_kernel(const uint16_t* __restrict__ X, const uint16_t* __restrict__ A, fl
         }
     }
 #pragma unroll
-    for (int m = 0; m < 16; ++m) {
+    for (int m = 0; m < kM; ++m) {
         if (m < M) {
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) t[m] += __shfl_xor_sync(0xffffffffu, t[m], o);
@@ -695,6 +712,52 @@ lora_t_kernel(const uint16_t* __restrict__ X, const uint16_t* __restrict__ A, fl
         float s = 0.f;
         for (int w = 0; w < kTThreads / 32; ++w) s += part[w][threadIdx.x];
         T[threadIdx.x * r + j] = s;
+    }
+}
+
+// Y[m][n] = bf16(sum of the slices' partial products, in slice order, + gamma
+// T[m] . B[n]): a thread per row n and four tokens.
+constexpr int kJoinTokens = 4;
+__global__ void __launch_bounds__(256)
+join_slices_kernel(const __grid_constant__ GemvFmtArgs a, int splits) {
+    grid_dependency_wait();                               // everything comes from the kernels before
+    const int64_t n = blockIdx.x * int64_t(blockDim.x) + threadIdx.x;
+    if (n >= a.N) return;
+    const int mb = blockIdx.y * kJoinTokens;
+    float s[kJoinTokens], l[kJoinTokens];
+#pragma unroll
+    for (int i = 0; i < kJoinTokens; ++i) {
+        s[i] = l[i] = 0.f;
+        if (mb + i < a.M) {
+            const float* part = a.part + int64_t(mb + i) * a.N + n;
+#pragma unroll 4
+            for (int k = 0; k < splits; ++k) s[i] += part[int64_t(k) * a.M * a.N];
+        }
+    }
+#pragma unroll 2
+    for (int j = 0; j < a.t_rank; j += 8) {
+        const uint4 bv = __ldg(reinterpret_cast<const uint4*>(a.B + n * a.t_rank + j));
+        const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
+#pragma unroll
+        for (int i = 0; i < kJoinTokens; ++i) {
+            if (mb + i < a.M) {
+                const float4* t = reinterpret_cast<const float4*>(a.T + (mb + i) * a.t_rank + j);
+                const float4 t0 = t[0], t1 = t[1];
+                const float tv[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    l[i] = fmaf(tv[2 * q], __uint_as_float(bw[q] << 16), l[i]);
+                    l[i] = fmaf(tv[2 * q + 1], __uint_as_float(bw[q] & 0xffff0000u), l[i]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kJoinTokens; ++i) {
+        if (mb + i < a.M) {
+            const __nv_bfloat16 y = __float2bfloat16_rn(fmaf(a.gamma, l[i], s[i]));
+            a.Y[(mb + i) * a.N + n] = *reinterpret_cast<const uint16_t*>(&y);
+        }
     }
 }
 
@@ -746,51 +809,75 @@ GemvFmtPlan gemv_fmt_plan(int M, int64_t N, int64_t K, int r, int log2_block, bo
     // Slices are whole multiples of 4 chunks: as few as leave their
     // activations the room.
     auto per_of = [&](int64_t splits) { return ((chunks + splits - 1) / splits + 3) / 4 * 4; };
-    auto key = [&](int64_t splits, int span) {
-        return PlanKey{M, static_cast<int>(std::min<int64_t>(per_of(splits), 1 << 20)), gran, r, log2_block, f32, span};
+    auto bytes = [&](int64_t splits, int warps_k, int64_t span) {
+        return plan_smem({M, static_cast<int>(std::min<int64_t>(per_of(splits), 1 << 20)), gran, r, log2_block, f32, warps_k,
+                          static_cast<int>(span)}).total;
     };
-    auto bytes = [&](int64_t splits, int64_t span) { return plan_smem(key(splits, static_cast<int>(span))).total; };
     int64_t splits = 1;
-    while (per_of(splits) > 4 && bytes(splits, 1) > kSmemLimit) ++splits;
+    // (many tokens: narrower slices, for the sake of L1: 8192 x 28672 with 16
+    // tokens 86.7 -> 80.9 us)
+    while (per_of(splits) > 4 && bytes(splits, kWarps, 1) > (M > 8 ? kSmemSmall : kSmemLimit)) ++splits;
     // few rows: more slices, as long as every warp keeps a step
     const int64_t by_rows = std::max<int64_t>(1, (N + 15) / 16);
-    while (by_rows * splits * 2 <= num_sms && per_of(splits * 2) >= 2 * kWarps && bytes(splits * 2, 1) <= kSmemLimit) splits *= 2;
+    while (by_rows * splits * 2 <= num_sms && per_of(splits * 2) >= 2 * kWarps) splits *= 2;
     GemvFmtPlan p;
     p.chunks = static_cast<int>(per_of(splits));
     p.splits = static_cast<int>((chunks + p.chunks - 1) / p.chunks);
     p.ctas = static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, num_sms / p.splits), by_rows));
+    // warps along the contraction: the least of the busiest warp's steps of
+    // 16 rows, and of its units of rows, which cost about two of them (with 16
+    // everywhere, 8192 x 28672 with 16 tokens took 149 us, so 108)
+    const int64_t rows = (N + p.ctas - 1) / p.ctas, steps = (p.chunks * 128 + kCols - 1) / kCols;
+    int64_t best = INT64_MAX;
+    p.warps_k = kWarps;
+    for (int w = kWarps; w >= 1; w /= 2) {
+        if (bytes(splits, w, 1) > kSmemLimit) continue;
+        const int64_t unit_rows = kRows * (kWarps / w), full = rows / unit_rows, rest = rows % unit_rows;
+        const int64_t cost = (2 * full + (rest > 16 ? 2 : rest > 0)) * ((steps + w - 1) / w) + 2 * (full + (rest > 0));
+        if (cost < best) {
+            best = cost;
+            p.warps_k = w;
+        }
+    }
     // rows of a CTA in as few equal spans as fit
-    const int64_t rows = (N + p.ctas - 1) / p.ctas;
-    const int unit_rows = plan_smem(key(splits, 1)).unit_rows;
-    const int64_t units = (rows + unit_rows - 1) / unit_rows;
-    const int64_t limit = std::max<int64_t>(bytes(splits, 1), kSmemSmall);
+    const int64_t unit_rows = kRows * (kWarps / p.warps_k), units = (rows + unit_rows - 1) / unit_rows;
+    const int64_t limit = std::max<int64_t>(bytes(splits, p.warps_k, 1), kSmemSmall);
     int64_t span = 1;
-    while (span < 64 && span < units && bytes(splits, span + 1) <= limit) ++span;
+    while (span < 64 && span < units && bytes(splits, p.warps_k, span + 1) <= limit) ++span;
     const int64_t spans = (units + span - 1) / span;
     p.span = static_cast<int>((units + spans - 1) / spans);
-    p.smem = static_cast<int>(bytes(splits, p.span));
+    p.smem = static_cast<int>(bytes(splits, p.warps_k, p.span));
     return p;
 }
 
 cudaError_t launch_gemv_fmt(GemvFmtArgs a, const GemvFmtPlan& p, cudaStream_t s) {
     const int gran = gran_of(a.log2_block, a.K);
     if (a.t_rank > 0) {
-        lora_t_kernel<<<static_cast<unsigned>(a.t_rank), kTThreads, 0, s>>>(a.X, a.A, a.T, a.M, a.K, a.t_rank);
+        auto* kernel = a.M == 1 ? lora_t_kernel<1> : a.M <= 4 ? lora_t_kernel<4> : lora_t_kernel<16>;
+        kernel<<<static_cast<unsigned>(a.t_rank), kTThreads, 0, s>>>(a.X, a.A, a.T, a.M, a.K, a.t_rank);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     a.chunks = p.chunks;
     a.span = p.span;
+    a.warps_k = p.warps_k;
     // a step's scales as whole words of one group, where each is a block of
     // its own and every row begins on a multiple of 4 steps' worth of them
     a.vec_scales = (1 << a.log2_block) == gran && a.K % std::max(kCols, 4 * gran) == 0;
     const dim3 grid(static_cast<unsigned>(p.ctas), static_cast<unsigned>(p.splits));
-    switch (gran) {
-        case 16: return run_gran<16>(a, grid, p.smem, s);
-        case 32: return run_gran<32>(a, grid, p.smem, s);
-        case 64: return run_gran<64>(a, grid, p.smem, s);
-        default: return run_gran<128>(a, grid, p.smem, s);
-    }
+    const cudaError_t e = gran == 16 ? run_gran<16>(a, grid, p.smem, s) : gran == 32 ? run_gran<32>(a, grid, p.smem, s)
+                          : gran == 64 ? run_gran<64>(a, grid, p.smem, s) : run_gran<128>(a, grid, p.smem, s);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((a.N + 255) / 256), static_cast<unsigned>((a.M + kJoinTokens - 1) / kJoinTokens));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_slices_kernel, a, p.splits);
 }
 
 }  // namespace qnf4

@@ -1534,10 +1534,6 @@ int qlora_linear_fmt_forward(const uint16_t* X, int64_t M, const uint8_t* packed
     a.scale_fmt = fa.scale_fmt;
     f16_codes(f, a.code, &a.code_undo);
     QTRY(launch_gemv_fmt(a, p, s));
-    if (p.splits > 1) {
-        GemvFinalizeArgs fin{a.part, a.T, p.splits, 1, B, r, scale, nullptr, Y, M, N};
-        QTRY(launch_gemv_finalize(fin, s));
-    }
     return QLORA_OK;
 }
 
