@@ -9,9 +9,15 @@
 // and memory cost") otherwise keeps only the layer's input and recomputes g
 // and u through two dequantising GEMMs.
 //
-// All four kernels are streams: a lane takes 8 values (one 16-byte word of
-// bf16, 8 bytes of codes), 8 lanes a block of 64, so the block's maximum is
-// three shuffles and every access is a full line of a warp.
+// All four kernels are streams bounded by HBM.  The writers take 16 values a
+// lane, so that a block's maximum is two shuffles and its constants (scale,
+// reciprocal) are formed by 4 lanes; with 8 values a lane, their arithmetic
+// took more time than the traffic (8192 x 11008, int8, us: copy 63 -> 46.8,
+// SwiGLU forward 186 -> 143).  The readers take 8, a 16-byte word of bf16.
+// Measured at 8192 x 11008, us, % of a 6568 GB/s copy: copy int8 46.8 (90%),
+// E4M3 47.0; reading back 48.3 (87%); SwiGLU forward 143 (78%: the division
+// of its sigmoid, which has to be the correctly rounded one for h to be the
+// h of the path without copies), backward 134 int8 (83%), 130 E4M3 (86%).
 #include "act8.cuh"
 
 namespace qnf4 {
@@ -22,21 +28,25 @@ constexpr int kThreads = 256;
 
 __device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
 
+// 16 values a lane: the block's constants are formed by 4 lanes in place of 8.
 template <int kCode>
 __global__ void __launch_bounds__(kThreads)
-act8_quantize_kernel(const uint4* __restrict__ X, uint2* __restrict__ codes, float* __restrict__ scales,
-                     int64_t n8) {
-    // n8 is a multiple of 8, so the 8 lanes of a block leave together; the
+act8_quantize_kernel(const uint4* __restrict__ X, uint4* __restrict__ codes, float* __restrict__ scales,
+                     int64_t n16) {
+    // n16 is a multiple of 4, so the 4 lanes of a block leave together; the
     // other lanes of the last warp still take part in the shuffles
-    for (int64_t i0 = blockIdx.x * int64_t(kThreads); i0 < n8; i0 += int64_t(gridDim.x) * kThreads) {
+    for (int64_t i0 = blockIdx.x * int64_t(kThreads); i0 < n16; i0 += int64_t(gridDim.x) * kThreads) {
         const int64_t i = i0 + threadIdx.x;
-        const bool live = i < n8;
-        const uint4 v = live ? __ldcs(X + i) : make_uint4(0u, 0u, 0u, 0u);
-        float s;
-        const uint2 c = act8_encode<kCode>(v, act8_absmax(v), &s);
-        if (!live) continue;
-        codes[i] = c;
-        if ((i & 7) == 0) scales[i >> 3] = s;
+        uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+        if (i < n16) {
+            v[0] = __ldcs(X + 2 * i);
+            v[1] = __ldcs(X + 2 * i + 1);
+        }
+        const Act8Block b = act8_block<kCode>(act8_block_max<4>(__vmaxu2(act8_absmax(v[0]), act8_absmax(v[1]))));
+        if (i >= n16) continue;
+        const uint2 lo = act8_codes<kCode>(v[0], b), hi = act8_codes<kCode>(v[1], b);
+        codes[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        if ((i & 3) == 0) scales[i >> 2] = b.s;
     }
 }
 
@@ -51,31 +61,41 @@ act8_dequantize_kernel(const uint2* __restrict__ codes, const float* __restrict_
 
 template <int kCode>
 __global__ void __launch_bounds__(kThreads)
-swiglu_forward_act8_kernel(const uint4* __restrict__ G, const uint4* __restrict__ U, uint4* __restrict__ H,
-                           uint2* __restrict__ g8, float* __restrict__ gs, uint2* __restrict__ u8,
-                           float* __restrict__ us, int64_t n8) {
-    for (int64_t i0 = blockIdx.x * int64_t(kThreads); i0 < n8; i0 += int64_t(gridDim.x) * kThreads) {
+swiglu_forward_act8_kernel(const uint4* G, const uint4* U, uint4* H,
+                           uint4* __restrict__ g8, float* __restrict__ gs, uint4* __restrict__ u8,
+                           float* __restrict__ us, int64_t n16) {
+    for (int64_t i0 = blockIdx.x * int64_t(kThreads); i0 < n16; i0 += int64_t(gridDim.x) * kThreads) {
         const int64_t i = i0 + threadIdx.x;
-        const bool live = i < n8;
-        const uint4 g = live ? __ldcs(G + i) : make_uint4(0u, 0u, 0u, 0u);
-        const uint4 u = live ? __ldcs(U + i) : make_uint4(0u, 0u, 0u, 0u);
-        float sg, su;
-        const uint2 cg = act8_encode<kCode>(g, act8_absmax(g), &sg);
-        const uint2 cu = act8_encode<kCode>(u, act8_absmax(u), &su);
-        if (!live) continue;
-        const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
-        uint32_t h[4];
+        uint4 g[2], u[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float g0 = bf16lo(gw[k]), g1 = bf16hi(gw[k]);
-            h[k] = pack_bf16x2(g0 * sigmoid(g0) * bf16lo(uw[k]), g1 * sigmoid(g1) * bf16hi(uw[k]));
+        for (int e = 0; e < 2; ++e) {
+            g[e] = u[e] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < n16) {
+                g[e] = __ldcs(G + 2 * i + e);
+                u[e] = __ldcs(U + 2 * i + e);
+            }
         }
-        __stcs(H + i, make_uint4(h[0], h[1], h[2], h[3]));
-        __stcs(g8 + i, cg);
-        __stcs(u8 + i, cu);
-        if ((i & 7) == 0) {
-            gs[i >> 3] = sg;
-            us[i >> 3] = su;
+        const Act8Block bg = act8_block<kCode>(act8_block_max<4>(__vmaxu2(act8_absmax(g[0]), act8_absmax(g[1]))));
+        const Act8Block bu = act8_block<kCode>(act8_block_max<4>(__vmaxu2(act8_absmax(u[0]), act8_absmax(u[1]))));
+        if (i >= n16) continue;
+        const uint2 g0 = act8_codes<kCode>(g[0], bg), g1 = act8_codes<kCode>(g[1], bg);
+        __stcs(g8 + i, make_uint4(g0.x, g0.y, g1.x, g1.y));
+        const uint2 u0 = act8_codes<kCode>(u[0], bu), u1 = act8_codes<kCode>(u[1], bu);
+        __stcs(u8 + i, make_uint4(u0.x, u0.y, u1.x, u1.y));
+        if ((i & 3) == 0) {
+            gs[i >> 2] = bg.s;
+            us[i >> 2] = bu.s;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t gw[4] = {g[e].x, g[e].y, g[e].z, g[e].w}, uw[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float z0 = bf16lo(gw[k]), z1 = bf16hi(gw[k]);
+                h[k] = pack_bf16x2(z0 * sigmoid(z0) * bf16lo(uw[k]), z1 * sigmoid(z1) * bf16hi(uw[k]));
+            }
+            __stcs(H + 2 * i + e, make_uint4(h[0], h[1], h[2], h[3]));
         }
     }
 }
@@ -144,13 +164,13 @@ cudaError_t swiglu_backward(const uint16_t* dH, const Act8View& g, const Act8Vie
 }  // namespace
 
 cudaError_t launch_act8_quantize(const uint16_t* X, const Act8View& o, int64_t n, int num_sms, cudaStream_t s) {
-    const unsigned grid = grid_for(n / 8, num_sms);
+    const unsigned grid = grid_for(n / 16, num_sms);
     const auto* x = reinterpret_cast<const uint4*>(X);
-    auto* c = reinterpret_cast<uint2*>(o.codes);
+    auto* c = reinterpret_cast<uint4*>(o.codes);
     if (o.code == QLORA_ACT8_E4M3)
-        act8_quantize_kernel<QLORA_ACT8_E4M3><<<grid, kThreads, 0, s>>>(x, c, o.scales, n / 8);
+        act8_quantize_kernel<QLORA_ACT8_E4M3><<<grid, kThreads, 0, s>>>(x, c, o.scales, n / 16);
     else
-        act8_quantize_kernel<QLORA_ACT8_INT8><<<grid, kThreads, 0, s>>>(x, c, o.scales, n / 8);
+        act8_quantize_kernel<QLORA_ACT8_INT8><<<grid, kThreads, 0, s>>>(x, c, o.scales, n / 16);
     return cudaGetLastError();
 }
 
@@ -167,14 +187,14 @@ cudaError_t launch_act8_dequantize(const Act8View& v, uint16_t* X, int64_t n, in
 
 cudaError_t launch_swiglu_forward_act8(const uint16_t* G, const uint16_t* U, uint16_t* H, const Act8View& g,
                                        const Act8View& u, int64_t n, int num_sms, cudaStream_t s) {
-    const unsigned grid = grid_for(n / 8, num_sms);
+    const unsigned grid = grid_for(n / 16, num_sms);
     const auto *pg = reinterpret_cast<const uint4*>(G), *pu = reinterpret_cast<const uint4*>(U);
     auto* h = reinterpret_cast<uint4*>(H);
-    auto *cg = reinterpret_cast<uint2*>(g.codes), *cu = reinterpret_cast<uint2*>(u.codes);
+    auto *cg = reinterpret_cast<uint4*>(g.codes), *cu = reinterpret_cast<uint4*>(u.codes);
     if (g.code == QLORA_ACT8_E4M3)
-        swiglu_forward_act8_kernel<QLORA_ACT8_E4M3><<<grid, kThreads, 0, s>>>(pg, pu, h, cg, g.scales, cu, u.scales, n / 8);
+        swiglu_forward_act8_kernel<QLORA_ACT8_E4M3><<<grid, kThreads, 0, s>>>(pg, pu, h, cg, g.scales, cu, u.scales, n / 16);
     else
-        swiglu_forward_act8_kernel<QLORA_ACT8_INT8><<<grid, kThreads, 0, s>>>(pg, pu, h, cg, g.scales, cu, u.scales, n / 8);
+        swiglu_forward_act8_kernel<QLORA_ACT8_INT8><<<grid, kThreads, 0, s>>>(pg, pu, h, cg, g.scales, cu, u.scales, n / 16);
     return cudaGetLastError();
 }
 

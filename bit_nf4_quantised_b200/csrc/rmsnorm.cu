@@ -124,12 +124,13 @@ rmsnorm_forward_kernel(RmsNormArgs a) {
             if (a.Y != nullptr && mine) __stcs(reinterpret_cast<uint4*>(a.Y + row * a.D + v * 8), yv);
             if (kCode >= 0) {
                 // D is a multiple of 64: a block's 8 lanes are all inside or all outside the row
-                float s;
-                const uint2 c = act8_encode<kCode < 0 ? 0 : kCode>(yv, act8_absmax(yv), &s);
+                constexpr int code = kCode < 0 ? 0 : kCode;
+                const Act8Block b = act8_block<code>(act8_block_max<8>(act8_absmax(yv)));
+                const uint2 c = act8_codes<code>(yv, b);
                 if (mine) {
                     const int64_t i = row * nvec + v;
                     __stcs(reinterpret_cast<uint2*>(a.q.codes) + i, c);
-                    if ((v & 7) == 0) a.q.scales[i >> 3] = s;
+                    if ((v & 7) == 0) a.q.scales[i >> 3] = b.s;
                 }
             }
         }
