@@ -10,11 +10,20 @@
 //
 // Both directions are streams bounded by HBM: forward 2 + 2 (+2) bytes read
 // and 2 + 2 (+1 1/16) written per element, backward 4 (+2) read, 2 written.
-// A row lives in registers (8 bf16 a lane and 16-byte word, NV words a lane),
-// so each tensor crosses HBM once.  Rows of up to 1024 values belong to a
-// warp, longer ones to a CTA.  The grid is persistent: a lane keeps its
-// columns of w (and of dw) in registers over all its rows, and the loads of
-// the next row are issued before the reduction of the current one.
+// Each tensor crosses HBM once: a row is spread over the lanes of a warp (up
+// to 1024 values) or a CTA, 8 bf16 a lane and 16-byte word, NV words a lane.
+// The grid is persistent: a lane keeps its columns of w (and of dw) in
+// registers over all its rows, and the next rows arrive by asynchronous copies
+// in a ring of shared memory, where each thread reads back only its own words.
+// (Held in registers instead, the next row left too few of them: backward
+// with residual and dw, 8192 x 4096, 69 us, so 46; 1024 x 16384, 334, so 31.)
+// Measured, us, % of a 6568 GB/s copy: 8192 x 4096 forward with residual 47.3
+// (86%), with the int8 copy 55.2 (84%); backward with residual and dw 46.4
+// (88%), without either 34.7 (88%); 513 x 1088 forward 2.6, backward 6.5;
+// 1 x 4096 forward 2.5.  1024 x 16384: forward 20.6 (99%), backward with
+// residual and dw 31.1 (66%: dw and its partial rows are as much as 160 rows).
+#include <algorithm>
+
 #include "act8.cuh"
 
 namespace qnf4 {
@@ -26,11 +35,7 @@ constexpr int kWarpRows = 8;           // warps (rows) of such a CTA
 constexpr int kMaxWidth = 16384;       // 512 lanes x 4 words x 8 values
 
 // Threads of the largest CTA that holds NV words of a row per lane.
-constexpr int max_threads(int nv) { return nv == 1 ? 1024 : 512; }
-
-__device__ __forceinline__ uint4 ldg_stream(const uint16_t* p) {
-    return __ldcs(reinterpret_cast<const uint4*>(p));
-}
+__host__ __device__ constexpr int max_threads(int nv) { return nv == 1 ? 1024 : 512; }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -50,30 +55,58 @@ __device__ __forceinline__ float row_sum(float v, float* buf, int nwarps) {
     return s;
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows in flight per row of threads in a kernel's ring, and its bytes.
+__host__ __device__ constexpr int pick(int nv, int s1, int s2, int s4) { return nv == 1 ? s1 : nv == 2 ? s2 : s4; }
+__host__ __device__ constexpr int forward_stages(int nv) { return pick(nv, 3, 2, 2); }
+__host__ __device__ constexpr int backward_stages(int nv) { return pick(nv, 4, 3, 2); }
+__host__ __device__ constexpr int forward_ring(int nv, bool res, int threads) {
+    return forward_stages(nv) * nv * (res ? 2 : 1) * 16 * threads;
+}
+__host__ __device__ constexpr int backward_ring(int nv, bool res, int threads) {
+    return backward_stages(nv) * nv * (res ? 3 : 2) * 16 * threads;
+}
+
 template <int NV, bool kRes, int kCode>      // kCode < 0: no 8-bit copy
 __global__ void __launch_bounds__(max_threads(NV))
 rmsnorm_forward_kernel(RmsNormArgs a) {
+    constexpr int S = forward_stages(NV), kTensors = kRes ? 2 : 1;
     __shared__ float red[2][32];
-    const int nvec = a.D / 8, lanes = blockDim.x, nwarps = lanes / 32;
+    extern __shared__ __align__(16) uint8_t ring[];
+    const int nvec = a.D / 8, lanes = blockDim.x, nwarps = lanes / 32, threads = blockDim.x * blockDim.y;
     const int64_t stride = int64_t(gridDim.x) * blockDim.y;
     int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
     const float inv_d = 1.0f / static_cast<float>(a.D);
 
-    float w[NV][8];
-    uint4 x[NV], r[NV];
-    auto load = [&](int64_t m) {
+    // The ring: [stage][word k][tensor][thread]; a thread reads back only what
+    // it copied itself, so its own wait is all the synchronisation there is.
+    uint8_t* const mine = ring + (threadIdx.y * lanes + threadIdx.x) * 16;
+    auto slot = [&](int stage, int k, int t) { return mine + ((stage * NV + k) * kTensors + t) * threads * 16; };
+    auto load = [&](int64_t m, int stage) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int v = threadIdx.x + k * lanes;
-            x[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (kRes) r[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (m < a.M && v < nvec) {
-                x[k] = ldg_stream(a.X + m * a.D + v * 8);
-                if (kRes) r[k] = ldg_stream(a.R + m * a.D + v * 8);
-            }
+            const bool in = m < a.M && v < nvec;
+            const int64_t at = in ? m * a.D + v * 8 : 0;
+            cp_async16(smem_u32(slot(stage, k, 0)), a.X + at, in ? 16 : 0);        // 0: zeros
+            if (kRes) cp_async16(smem_u32(slot(stage, k, 1)), a.R + at, in ? 16 : 0);
         }
+        cp_async_commit();
     };
-    load(row);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+        if (row + i * stride < a.M) load(row + i * stride, i);
+        else cp_async_commit();
+    }
+    float w[NV][8];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int v = threadIdx.x + k * lanes;
@@ -85,14 +118,19 @@ rmsnorm_forward_kernel(RmsNormArgs a) {
         w[k][0] = lo.x; w[k][1] = lo.y; w[k][2] = lo.z; w[k][3] = lo.w;
         w[k][4] = hi.x; w[k][5] = hi.y; w[k][6] = hi.z; w[k][7] = hi.w;
     }
+    int stage = 0;
     // rows of a CTA leave the loop together, so its barriers stay aligned
     for (int it = 0; row - threadIdx.y < a.M; row += stride, ++it) {
+        load(row + (S - 1) * stride, stage == 0 ? S - 1 : stage - 1);
+        cp_async_wait<S - 1>();
         uint32_t h[NV][4];
         float ss = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const uint32_t xw[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            const uint32_t rw[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+            const uint4 x = *reinterpret_cast<const uint4*>(slot(stage, k, 0));
+            uint4 r = make_uint4(0u, 0u, 0u, 0u);
+            if (kRes) r = *reinterpret_cast<const uint4*>(slot(stage, k, 1));
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, rw[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 h[k][j] = kRes ? pack_bf16x2(bf16lo(xw[j]) + bf16lo(rw[j]), bf16hi(xw[j]) + bf16hi(rw[j])) : xw[j];
@@ -110,7 +148,6 @@ rmsnorm_forward_kernel(RmsNormArgs a) {
                            make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]));
             }
         }
-        load(row + stride);
         const float rstd = __frsqrt_rn(fmaf(row_sum(ss, red[it & 1], nwarps), inv_d, a.eps));
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -134,35 +171,53 @@ rmsnorm_forward_kernel(RmsNormArgs a) {
                 }
             }
         }
+        stage = stage == S - 1 ? 0 : stage + 1;
     }
+    cp_async_wait<0>();
+}
+
+// A load that the compiler does not replace by the registers of an earlier one.
+__device__ __forceinline__ uint4 lds_again(const void* p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(smem_u32(p)));
+    return v;
 }
 
 template <int NV, bool kRes, bool kWeight>
 __global__ void __launch_bounds__(max_threads(NV))
 rmsnorm_backward_kernel(RmsNormGradArgs a) {
+    constexpr int S = backward_stages(NV), kTensors = kRes ? 3 : 2;
     __shared__ float red[2][2][32];
-    const int nvec = a.D / 8, lanes = blockDim.x, nwarps = lanes / 32;
+    extern __shared__ __align__(16) uint8_t ring[];
+    const int nvec = a.D / 8, lanes = blockDim.x, nwarps = lanes / 32, threads = blockDim.x * blockDim.y;
     const int64_t stride = int64_t(gridDim.x) * blockDim.y;
     int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
     const float inv_d = 1.0f / static_cast<float>(a.D);
     launch_dependents();                         // the sum of the partial dw waits for this grid
 
-    float w[NV][8], dw[NV][8];
-    uint4 g[NV], x[NV], r[NV];
-    auto load = [&](int64_t m) {
+    // The ring: [stage][word k][tensor][thread]; a thread reads back only what
+    // it copied itself, so its own wait is all the synchronisation there is.
+    uint8_t* const mine = ring + (threadIdx.y * lanes + threadIdx.x) * 16;
+    auto slot = [&](int stage, int k, int t) { return mine + ((stage * NV + k) * kTensors + t) * threads * 16; };
+    auto load = [&](int64_t m, int stage) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int v = threadIdx.x + k * lanes;
-            g[k] = x[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (kRes) r[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (m < a.M && v < nvec) {
-                g[k] = ldg_stream(a.dY + m * a.D + v * 8);
-                x[k] = ldg_stream(a.H + m * a.D + v * 8);
-                if (kRes) r[k] = ldg_stream(a.dR + m * a.D + v * 8);
-            }
+            const bool in = m < a.M && v < nvec;
+            const int64_t at = in ? m * a.D + v * 8 : 0;
+            cp_async16(smem_u32(slot(stage, k, 0)), a.dY + at, in ? 16 : 0);       // 0: zeros
+            cp_async16(smem_u32(slot(stage, k, 1)), a.H + at, in ? 16 : 0);
+            if (kRes) cp_async16(smem_u32(slot(stage, k, 2)), a.dR + at, in ? 16 : 0);
         }
+        cp_async_commit();
     };
-    load(row);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+        if (row + i * stride < a.M) load(row + i * stride, i);
+        else cp_async_commit();
+    }
+    float w[NV][8], dw[NV][8];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int v = threadIdx.x + k * lanes;
@@ -176,15 +231,17 @@ rmsnorm_backward_kernel(RmsNormGradArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[k][j] = 0.f;
     }
+    int stage = 0;
     for (int it = 0; row - threadIdx.y < a.M; row += stride, ++it) {
-        uint4 gc[NV], xc[NV], rc[NV];
+        load(row + (S - 1) * stride, stage == 0 ? S - 1 : stage - 1);
+        cp_async_wait<S - 1>();
+        uint4 gc[NV], xc[NV];
         float ss = 0.f, st = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            gc[k] = g[k];
-            xc[k] = x[k];
-            if (kRes) rc[k] = r[k];
-            const uint32_t gw[4] = {g[k].x, g[k].y, g[k].z, g[k].w}, xw[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            gc[k] = *reinterpret_cast<const uint4*>(slot(stage, k, 0));
+            xc[k] = *reinterpret_cast<const uint4*>(slot(stage, k, 1));
+            const uint32_t gw[4] = {gc[k].x, gc[k].y, gc[k].z, gc[k].w}, xw[4] = {xc[k].x, xc[k].y, xc[k].z, xc[k].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float h0 = bf16lo(xw[j]), h1 = bf16hi(xw[j]);
@@ -194,7 +251,6 @@ rmsnorm_backward_kernel(RmsNormGradArgs a) {
                 st = fmaf(bf16hi(gw[j]) * w[k][2 * j + 1], h1, st);
             }
         }
-        load(row + stride);
         ss = warp_sum(ss);
         st = warp_sum(st);
         if (nwarps > 1) {
@@ -216,8 +272,14 @@ rmsnorm_backward_kernel(RmsNormGradArgs a) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int v = threadIdx.x + k * lanes;
+            if (NV == 4 && kWeight) {            // no registers to keep them in
+                gc[k] = lds_again(slot(stage, k, 0));
+                xc[k] = lds_again(slot(stage, k, 1));
+            }
             const uint32_t gw[4] = {gc[k].x, gc[k].y, gc[k].z, gc[k].w}, xw[4] = {xc[k].x, xc[k].y, xc[k].z, xc[k].w};
-            const uint32_t rw[4] = {rc[k].x, rc[k].y, rc[k].z, rc[k].w};
+            uint4 rc = make_uint4(0u, 0u, 0u, 0u);
+            if (kRes) rc = *reinterpret_cast<const uint4*>(slot(stage, k, 2));
+            const uint32_t rw[4] = {rc.x, rc.y, rc.z, rc.w};
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -236,12 +298,15 @@ rmsnorm_backward_kernel(RmsNormGradArgs a) {
             if (live && v < nvec)
                 __stcs(reinterpret_cast<uint4*>(a.dX + row * a.D + v * 8), make_uint4(o[0], o[1], o[2], o[3]));
         }
+        stage = stage == S - 1 ? 0 : stage + 1;
     }
+    cp_async_wait<0>();
     if (!kWeight) return;
     // one partial row of dw per CTA; the warps of a warp-per-row CTA add
     // theirs in warp order through shared memory
-    extern __shared__ float sdw[];
+    float* const sdw = reinterpret_cast<float*>(ring);
     if (blockDim.y > 1) {
+        __syncthreads();                         // every thread is done with its part of the ring
         if (threadIdx.y > 0) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
@@ -270,20 +335,23 @@ rmsnorm_backward_kernel(RmsNormGradArgs a) {
 }
 
 // dw = (accumulate ? dw : 0) + the sum of the partial rows.  A CTA takes 32
-// columns; its 8 warps add interleaved rows and then, in warp order, one
+// columns; its warps add interleaved rows and then, in warp order, one
 // another's sums: a fixed order.
-__global__ void __launch_bounds__(256)
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(kSumWarps * 32)
 rmsnorm_dweight_kernel(const float* __restrict__ part, int parts, int D, float* dweight, int accumulate) {
-    __shared__ float s[8][32];
+    __shared__ float s[kSumWarps][32];
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
     float t = 0.f;
-    if (col < D)
-        for (int p = warp; p < parts; p += 8) t += part[int64_t(p) * D + col];
+    if (col < D) {
+#pragma unroll 8
+        for (int p = warp; p < parts; p += kSumWarps) t += part[int64_t(p) * D + col];
+    }
     s[warp][lane] = t;
     __syncthreads();
     if (warp == 0 && col < D) {
-        for (int q = 1; q < 8; ++q) t += s[q][lane];
+        for (int q = 1; q < kSumWarps; ++q) t += s[q][lane];
         dweight[col] = accumulate ? dweight[col] + t : t;
     }
 }
@@ -320,36 +388,45 @@ unsigned grid_for(const Shape& s, int num_sms, int threads_per_sm) {
     return static_cast<unsigned>(s.rows_ctas < cap ? s.rows_ctas : cap);
 }
 
-constexpr int kForwardThreads = 768;    // per SM
+// Threads per SM that a kernel's registers and ring allow, taken over by its
+// persistent grid: forward 1024, or 512 where a lane holds four words of a
+// CTA's row.  (8192 x 4096 with 768: 49 us and 1024: 47; the backward with
+// residual and dw with 512: 46, 768: 55, 1024: 49.)
+int forward_threads(const Shape& s) { return s.nv == 4 && s.block.y == 1 ? 512 : 1024; }
 constexpr int kBackwardThreads = 512;
 
 template <int NV, bool kRes>
-void run_forward(const RmsNormArgs& a, const Shape& s, unsigned grid, cudaStream_t st) {
-    if (a.q.codes == nullptr)
-        rmsnorm_forward_kernel<NV, kRes, -1><<<grid, s.block, 0, st>>>(a);
-    else if (a.q.code == QLORA_ACT8_E4M3)
-        rmsnorm_forward_kernel<NV, kRes, QLORA_ACT8_E4M3><<<grid, s.block, 0, st>>>(a);
-    else
-        rmsnorm_forward_kernel<NV, kRes, QLORA_ACT8_INT8><<<grid, s.block, 0, st>>>(a);
+cudaError_t run_forward(const RmsNormArgs& a, const Shape& s, unsigned grid, cudaStream_t st) {
+    const int smem = forward_ring(NV, kRes, static_cast<int>(s.block.x * s.block.y));
+    auto* kernel = a.q.codes == nullptr ? rmsnorm_forward_kernel<NV, kRes, -1>
+                   : a.q.code == QLORA_ACT8_E4M3 ? rmsnorm_forward_kernel<NV, kRes, QLORA_ACT8_E4M3>
+                                                 : rmsnorm_forward_kernel<NV, kRes, QLORA_ACT8_INT8>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, s.block, smem, st>>>(a);
+    return cudaGetLastError();
 }
 
 template <int NV>
-void run_forward(const RmsNormArgs& a, const Shape& s, unsigned grid, cudaStream_t st) {
-    if (a.R != nullptr) run_forward<NV, true>(a, s, grid, st);
-    else run_forward<NV, false>(a, s, grid, st);
+cudaError_t run_forward(const RmsNormArgs& a, const Shape& s, unsigned grid, cudaStream_t st) {
+    return a.R != nullptr ? run_forward<NV, true>(a, s, grid, st) : run_forward<NV, false>(a, s, grid, st);
 }
 
 template <int NV, bool kRes>
-void run_backward(const RmsNormGradArgs& a, const Shape& s, unsigned grid, cudaStream_t st) {
-    const size_t smem = a.dweight && s.block.y > 1 ? size_t(s.block.y - 1) * a.D * 4 : 0;
-    if (a.dweight) rmsnorm_backward_kernel<NV, kRes, true><<<grid, s.block, smem, st>>>(a);
-    else rmsnorm_backward_kernel<NV, kRes, false><<<grid, s.block, 0, st>>>(a);
+cudaError_t run_backward(const RmsNormGradArgs& a, const Shape& s, unsigned grid, cudaStream_t st) {
+    // the ring; at the end the partial dw of all rows of threads but one
+    const int threads = static_cast<int>(s.block.x * s.block.y);
+    const int smem = std::max(backward_ring(NV, kRes, threads), static_cast<int>(s.block.y - 1) * a.D * 4);
+    auto* kernel = a.dweight ? rmsnorm_backward_kernel<NV, kRes, true> : rmsnorm_backward_kernel<NV, kRes, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, s.block, smem, st>>>(a);
+    return cudaGetLastError();
 }
 
 template <int NV>
-void run_backward(const RmsNormGradArgs& a, const Shape& s, unsigned grid, cudaStream_t st) {
-    if (a.dR != nullptr) run_backward<NV, true>(a, s, grid, st);
-    else run_backward<NV, false>(a, s, grid, st);
+cudaError_t run_backward(const RmsNormGradArgs& a, const Shape& s, unsigned grid, cudaStream_t st) {
+    return a.dR != nullptr ? run_backward<NV, true>(a, s, grid, st) : run_backward<NV, false>(a, s, grid, st);
 }
 
 }  // namespace
@@ -362,28 +439,20 @@ int rmsnorm_parts(int64_t M, int D, int num_sms) {
 
 cudaError_t launch_rmsnorm_forward(const RmsNormArgs& a, int num_sms, cudaStream_t st) {
     const Shape s = shape_for(a.M, a.D, num_sms);
-    const unsigned grid = grid_for(s, num_sms, kForwardThreads);
-    switch (s.nv) {
-        case 1: run_forward<1>(a, s, grid, st); break;
-        case 2: run_forward<2>(a, s, grid, st); break;
-        default: run_forward<4>(a, s, grid, st); break;
-    }
-    return cudaGetLastError();
+    const unsigned grid = grid_for(s, num_sms, forward_threads(s));
+    return s.nv == 1 ? run_forward<1>(a, s, grid, st)
+           : s.nv == 2 ? run_forward<2>(a, s, grid, st) : run_forward<4>(a, s, grid, st);
 }
 
 cudaError_t launch_rmsnorm_backward(const RmsNormGradArgs& a, int num_sms, cudaStream_t st) {
     const Shape s = shape_for(a.M, a.D, num_sms);
     const unsigned grid = grid_for(s, num_sms, kBackwardThreads);
-    switch (s.nv) {
-        case 1: run_backward<1>(a, s, grid, st); break;
-        case 2: run_backward<2>(a, s, grid, st); break;
-        default: run_backward<4>(a, s, grid, st); break;
-    }
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = s.nv == 1 ? run_backward<1>(a, s, grid, st)
+                          : s.nv == 2 ? run_backward<2>(a, s, grid, st) : run_backward<4>(a, s, grid, st);
     if (e != cudaSuccess || a.dweight == nullptr) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((a.D + 31) / 32));
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(kSumWarps * 32);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
