@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -684,19 +685,20 @@ def _raw_stream() -> int:
 
 
 def _arg(t: torch.Tensor, dtype, shape, dev, name: str) -> int:
-    """Pointer of a contiguous tensor of this type, shape and device."""
-    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}"
-                         f"{'' if t.is_contiguous() else ' (not contiguous)'}")
-    return t.data_ptr()
+    """Pointer of a contiguous tensor of this type, shape and (CUDA) device."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == dev:
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
+                     f"{t.dtype} {tuple(t.shape)} on {t.device}"
+                     f"{'' if t.is_contiguous() else ' (not contiguous)'}")
 
 
 def _matrix(t: torch.Tensor, name: str):
     """(rows, cols, device) of a contiguous 2-D bf16 CUDA tensor."""
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
+    shape = t.shape
+    if t.dtype is not torch.bfloat16 or len(shape) != 2 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 2-D CUDA torch.bfloat16 tensor")
-    return t.shape[0], t.shape[1], t.device
+    return shape[0], shape[1], t.device
 
 
 @dataclass
@@ -718,12 +720,13 @@ class Act8:
         if (rows is not None and r != rows) or (cols is not None and c != cols):
             raise ValueError(f"{name} is {r} x {c}, expected {r if rows is None else rows} x "
                              f"{c if cols is None else cols}")
-        for t, n, what in ((self.codes, r * c, "codes"), (self.scales, r * c // ACT8_BLOCK, "scales")):
-            if t.numel() != n or not t.is_contiguous() or not t.is_cuda or t.device != dev:
+        codes, scales = self.codes, self.scales
+        for t, n, what in ((codes, r * c, "codes"), (scales, r * c // ACT8_BLOCK, "scales")):
+            if t.numel() != n or t.device != dev or not t.is_contiguous():
                 raise ValueError(f"{name}.{what} must be a contiguous tensor of {n} values on {dev}")
-        if self.codes.element_size() != 1 or self.scales.dtype != torch.float32:
-            raise ValueError(f"{name}: codes are one byte each, scales torch.float32")
-        return _Act8(self.codes.data_ptr(), self.scales.data_ptr(), r, c, self.code)
+        if codes.element_size() != 1 or scales.dtype is not torch.float32 or not codes.is_cuda:
+            raise ValueError(f"{name}: CUDA tensors, codes one byte each, scales torch.float32")
+        return _Act8(codes.data_ptr(), scales.data_ptr(), r, c, self.code)
 
 
 def qlora_act8_sizes(rows: int, cols: int):
@@ -736,9 +739,9 @@ def qlora_act8_sizes(rows: int, cols: int):
 def empty_act8(rows: int, cols: int, code: int = QLORA_ACT8_INT8, device="cuda") -> Act8:
     if rows < 0 or cols < 0 or cols % ACT8_BLOCK:
         qlora_act8_sizes(rows, cols)       # raises what the library says of these sizes
-    dt = torch.float8_e4m3fn if code == QLORA_ACT8_E4M3 else torch.int8
-    return Act8(torch.empty(rows * cols, dtype=dt, device=device),
-                torch.empty(rows * cols // ACT8_BLOCK, dtype=torch.float32, device=device), rows, cols, code)
+    codes = torch.empty(rows * cols, dtype=torch.float8_e4m3fn if code == QLORA_ACT8_E4M3 else torch.int8,
+                        device=device)
+    return Act8(codes, codes.new_empty(rows * cols // ACT8_BLOCK, dtype=torch.float32), rows, cols, code)
 
 
 def qlora_act8_quantize(X: torch.Tensor, code: int = QLORA_ACT8_INT8, out: Act8 | None = None,
@@ -798,8 +801,11 @@ def qlora_swiglu_backward_act8(dH: torch.Tensor, g8: Act8, u8: Act8, dG: torch.T
     return dG, dU
 
 
+_quantized_sizes = functools.lru_cache(maxsize=1024)(qlora_quantized_sizes)
+
+
 def _nf4_struct(w: NF4Tensor, dev, name: str) -> _Tensor:
-    p, c, m = qlora_quantized_sizes(w.rows, w.cols)
+    p, c, m = _quantized_sizes(w.rows, w.cols)
     for t, n, what in ((w.packed, p, "packed"), (w.scale_codes, c, "scale_codes"),
                        (w.meta_scale, m // 4, "meta_scale")):
         if t.numel() < n or t.device != dev or not t.is_contiguous():
@@ -965,6 +971,11 @@ def qlora_rmsnorm_workspace_size(M: int, D: int) -> int:
     return b.value
 
 
+@functools.lru_cache(maxsize=1024)
+def _rmsnorm_workspace(M: int, D: int, device: int) -> int:
+    return qlora_rmsnorm_workspace_size(M, D)         # of the current device: its number of SMs
+
+
 def qlora_rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Tensor, eps: float,
                            dres: torch.Tensor | None = None, dX: torch.Tensor | None = None,
                            dweight: torch.Tensor | None = None, want_dweight: bool = True,
@@ -984,9 +995,9 @@ def qlora_rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Tens
         elif dweight is None:
             if accumulate:
                 raise ValueError("accumulate needs dweight")
-            dweight = torch.empty(D, dtype=f32, device=dev)
+            dweight = dY.new_empty(D, dtype=f32)
         if dweight is not None:
-            ws = _workspace(ws, qlora_rmsnorm_workspace_size(M, D) if ws is None else 0, dev)
+            ws = _workspace(ws, _rmsnorm_workspace(M, D, dev.index) if ws is None else 0, dev)
         _check(lib().qlora_rmsnorm_backward(
             dY.data_ptr(), ph, pr, pw, M, D, eps, _arg(dX, bf, dY.shape, dev, "dX"),
             None if dweight is None else _arg(dweight, f32, (D,), dev, "dweight"), int(bool(accumulate)),
@@ -998,6 +1009,19 @@ def qlora_rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Tens
 def qlora_linear_fmt_workspace_size(M: int, N: int, K: int, r: int, fmt: Format) -> int:
     b = ctypes.c_size_t()
     _check(lib().qlora_linear_fmt_workspace_size(M, N, K, r, fmt.c_struct(), ctypes.byref(b)),
+           "qlora_linear_fmt_workspace_size")
+    return b.value
+
+
+@functools.lru_cache(maxsize=256)
+def _format_struct(codes: tuple, block: int, scales: int) -> _Format:
+    return Format(codes, block, scales).c_struct()
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_fmt_workspace(M: int, N: int, K: int, r: int, codes: tuple, block: int, scales: int, device: int) -> int:
+    b = ctypes.c_size_t()                             # of the current device: its number of SMs
+    _check(lib().qlora_linear_fmt_workspace_size(M, N, K, r, _format_struct(codes, block, scales), ctypes.byref(b)),
            "qlora_linear_fmt_workspace_size")
     return b.value
 
@@ -1016,21 +1040,20 @@ def qlora_linear_fmt_forward(X: torch.Tensor, packed: torch.Tensor, scales: torc
     blocks = -(-N * K // fmt.block)
     f32 = fmt.scales == QLORA_SCALES_FP32
     with _on(X, stream):
-        Y = Y if Y is not None else torch.empty(M, N, dtype=bf, device=dev)
-        st = fmt.c_struct()
+        codes = tuple(fmt.codes)
+        st = _format_struct(codes, fmt.block, fmt.scales)
         if ws is None:
-            b = ctypes.c_size_t()
-            _check(lib().qlora_linear_fmt_workspace_size(M, N, K, r, st, ctypes.byref(b)),
-                   "qlora_linear_fmt_workspace_size")
-            ws = torch.empty(b.value, dtype=torch.uint8, device=dev)
+            size = _linear_fmt_workspace(M, N, K, r, codes, fmt.block, fmt.scales, dev.index)
+            ws = X.new_empty(size, dtype=torch.uint8) if size else None
         else:
             _workspace(ws, 0, dev)
+        Y = Y if Y is not None else X.new_empty(M, N)
         _check(lib().qlora_linear_fmt_forward(
             X.data_ptr(), M, _arg(packed, torch.uint8, (blocks * fmt.block // 2,), dev, "packed"),
             _arg(scales, torch.float32 if f32 else torch.uint8, (blocks,), dev, "scales"),
             None if f32 else _arg(meta, torch.float32, (-(-blocks // GROUP),), dev, "meta"), N, K, st,
             None if A is None else _arg(A, bf, (r, K), dev, "A"),
             None if B is None else _arg(B, bf, (N, r), dev, "B"), r, float(scale),
-            _arg(Y, bf, (M, N), dev, "Y"), ws.data_ptr(), ws.nbytes, _raw_stream()),
-            "qlora_linear_fmt_forward")
+            _arg(Y, bf, (M, N), dev, "Y"), None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
+            _raw_stream()), "qlora_linear_fmt_forward")
     return Y

@@ -1442,6 +1442,7 @@ void f16_codes(const qlora_format* f, uint16_t code[16], float* undo) {
     const double unit = std::ldexp(1.0, -std::ilogb(top));
     double best = std::numeric_limits<double>::infinity();
     for (const int k : {1, 3, 5, 7, 15}) {
+        if (best == 0.0) break;
         uint16_t h[16] = {};
         double err = 0.0;
         for (int i = 0; i < f->ncodes; ++i) {
