@@ -108,7 +108,7 @@ struct PlanKey {
 // loads of a chunk's entries meet no bank twice.
 __host__ __device__ constexpr int scale_pitch(int gran) { return gran == 128 ? 2 : gran == 64 ? 6 : 256 / gran + 4; }
 
-__host__ __device__ inline Plan plan_smem(const PlanKey& k) {
+inline Plan plan_smem(const PlanKey& k) {
     Plan p;
     p.unit_rows = kRows * (kWarps / k.warps_k);
     p.span_rows = k.span * p.unit_rows;
@@ -174,7 +174,7 @@ __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32
 // columns, else exchanged words.  NT: tiles of 8 tokens (1 with kCol).
 template <int kGran, bool kCol, int NT, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
-gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a) {
+gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ Plan p) {
     constexpr int kPer = 128 / kGran;                     // scales of a row and chunk
     constexpr int E = kCols / kGran;                      // of a step
     constexpr int kPitch = scale_pitch(kGran);
@@ -188,19 +188,20 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a) {
     const int M = a.M;
     const int64_t k_beg = int64_t(blockIdx.y) * a.chunks * 128;
     const int kslab = static_cast<int>(min(K - k_beg, int64_t(a.chunks) * 128));
-    const Plan p = plan_smem({M, a.chunks, kGran, a.t_rank, a.log2_block, kF32, a.warps_k, a.span});
     float* const scales = reinterpret_cast<float*>(smem + p.scales) + warp * kRows * kPitch;
     uint32_t* const smax = reinterpret_cast<uint32_t*>(smem + p.misc);
     float* const sundo = reinterpret_cast<float*>(smem + p.misc + 64);
 
     // rows of this CTA, and this warp's part of a unit: 32 rows (the wr-th
     // such group of the unit) x steps m0 ... m1 - 1
-    const int64_t r0 = a.N * blockIdx.x / gridDim.x, r1 = a.N * (blockIdx.x + 1) / gridDim.x;
-    const int warps_k = a.warps_k, unit_rows = p.unit_rows;
-    const int wk = warp & (warps_k - 1), wr = warp / warps_k;
-    const int units = static_cast<int>((r1 - r0 + unit_rows - 1) / unit_rows);
+    // (no division here: the first loads wait for these)
+    const int64_t r0 = blockIdx.x * a.rows + min(int64_t(blockIdx.x), a.extra);
+    const int64_t r1 = r0 + a.rows + (int64_t(blockIdx.x) < a.extra ? 1 : 0);
+    const int warps_k = 1 << a.log2_warps, unit_rows = p.unit_rows;
+    const int wk = warp & (warps_k - 1), wr = warp >> a.log2_warps;
+    const int units = static_cast<int>(r1 - r0 + unit_rows - 1) >> (9 - a.log2_warps);      // 32 x 16 rows / warps_k
     const int steps = (kslab + kCols - 1) / kCols;
-    const int m0 = steps * wk / warps_k, m1 = steps * (wk + 1) / warps_k;
+    const int m0 = steps * wk >> a.log2_warps, m1 = steps * (wk + 1) >> a.log2_warps;
     auto rows_in = [&](int u) {
         const int64_t left = r1 - (r0 + int64_t(u) * unit_rows + wr * kRows);
         return static_cast<int>(min(left, int64_t(kRows)));
@@ -762,7 +763,8 @@ join_slices_kernel(const __grid_constant__ GemvFmtArgs a, int splits) {
 }
 
 template <int kGran, bool kCol, int NT, bool kF32>
-cudaError_t run(const GemvFmtArgs& a, dim3 grid, int smem, cudaStream_t s) {
+cudaError_t run(const GemvFmtArgs& a, const Plan& p, dim3 grid, cudaStream_t s) {
+    const int smem = static_cast<int>(p.total);
     auto* kernel = gemv_fmt_kernel<kGran, kCol, NT, kF32>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -776,22 +778,22 @@ cudaError_t run(const GemvFmtArgs& a, dim3 grid, int smem, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.t_rank > 0 ? 1 : 0;      // after lora_t_kernel
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a, p);
 }
 
 template <int kGran, bool kCol, int NT>
-cudaError_t run_scales(const GemvFmtArgs& a, dim3 grid, int smem, cudaStream_t s) {
-    return a.scale_fmt == QLORA_SCALES_FP32 ? run<kGran, kCol, NT, true>(a, grid, smem, s)
-                                            : run<kGran, kCol, NT, false>(a, grid, smem, s);
+cudaError_t run_scales(const GemvFmtArgs& a, const Plan& p, dim3 grid, cudaStream_t s) {
+    return a.scale_fmt == QLORA_SCALES_FP32 ? run<kGran, kCol, NT, true>(a, p, grid, s)
+                                            : run<kGran, kCol, NT, false>(a, p, grid, s);
 }
 
 // (token, block) columns where one tile of 8 holds them all
 template <int kGran>
-cudaError_t run_gran(const GemvFmtArgs& a, dim3 grid, int smem, cudaStream_t s) {
+cudaError_t run_gran(const GemvFmtArgs& a, const Plan& p, dim3 grid, cudaStream_t s) {
     if constexpr (kGran < 128) {
-        if (a.M <= (kGran == 64 ? 4 : 2)) return run_scales<kGran, true, 1>(a, grid, smem, s);
+        if (a.M <= (kGran == 64 ? 4 : 2)) return run_scales<kGran, true, 1>(a, p, grid, s);
     }
-    return a.M <= 8 ? run_scales<kGran, false, 1>(a, grid, smem, s) : run_scales<kGran, false, 2>(a, grid, smem, s);
+    return a.M <= 8 ? run_scales<kGran, false, 1>(a, p, grid, s) : run_scales<kGran, false, 2>(a, p, grid, s);
 }
 
 // Columns that share a scale: the block, up to a chunk.  Rows of an odd
@@ -846,7 +848,6 @@ GemvFmtPlan gemv_fmt_plan(int M, int64_t N, int64_t K, int r, int log2_block, bo
     while (span < 64 && span < units && bytes(splits, p.warps_k, span + 1) <= limit) ++span;
     const int64_t spans = (units + span - 1) / span;
     p.span = static_cast<int>((units + spans - 1) / spans);
-    p.smem = static_cast<int>(bytes(splits, p.warps_k, p.span));
     return p;
 }
 
@@ -860,13 +861,17 @@ cudaError_t launch_gemv_fmt(GemvFmtArgs a, const GemvFmtPlan& p, cudaStream_t s)
     }
     a.chunks = p.chunks;
     a.span = p.span;
-    a.warps_k = p.warps_k;
+    a.log2_warps = 0;
+    while ((1 << a.log2_warps) < p.warps_k) ++a.log2_warps;
+    a.rows = a.N / p.ctas;
+    a.extra = a.N % p.ctas;
+    const Plan sp = plan_smem({a.M, p.chunks, gran, a.t_rank, a.log2_block, a.scale_fmt == QLORA_SCALES_FP32, p.warps_k, p.span});
     // a step's scales as whole words of one group, where each is a block of
     // its own and every row begins on a multiple of 4 steps' worth of them
     a.vec_scales = (1 << a.log2_block) == gran && a.K % std::max(kCols, 4 * gran) == 0;
     const dim3 grid(static_cast<unsigned>(p.ctas), static_cast<unsigned>(p.splits));
-    const cudaError_t e = gran == 16 ? run_gran<16>(a, grid, p.smem, s) : gran == 32 ? run_gran<32>(a, grid, p.smem, s)
-                          : gran == 64 ? run_gran<64>(a, grid, p.smem, s) : run_gran<128>(a, grid, p.smem, s);
+    const cudaError_t e = gran == 16 ? run_gran<16>(a, sp, grid, s) : gran == 32 ? run_gran<32>(a, sp, grid, s)
+                          : gran == 64 ? run_gran<64>(a, sp, grid, s) : run_gran<128>(a, sp, grid, s);
     if (e != cudaSuccess || p.splits == 1) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((a.N + 255) / 256), static_cast<unsigned>((a.M + kJoinTokens - 1) / kJoinTokens));

@@ -257,12 +257,13 @@ struct GemvFmtArgs {
     uint16_t code[16];         // f16 bits of code * factor
     float code_undo;           // 1 / factor
     int chunks;                // 128-wide chunks per contraction slice (the rest by launch_gemv_fmt)
-    int warps_k;               // warps along a slice, a power of two
+    int64_t rows, extra;       // rows per CTA, and how many CTAs take one more
+    int log2_warps;            // log2 of the warps along a slice
     int span;                  // units of rows between barriers
     int vec_scales;
 };
 struct GemvFmtPlan {
-    int splits, chunks, ctas, warps_k, span, smem;
+    int splits, chunks, ctas, warps_k, span;
 };
 GemvFmtPlan gemv_fmt_plan(int M, int64_t N, int64_t K, int r, int log2_block, bool f32, int num_sms);
 cudaError_t launch_gemv_fmt(GemvFmtArgs a, const GemvFmtPlan& p, cudaStream_t s);
