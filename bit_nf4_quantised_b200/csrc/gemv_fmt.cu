@@ -86,10 +86,15 @@ constexpr int kLutBytes = 256 * 256;         // 256 byte values, 64 words apart,
 constexpr int kRows = 32;                    // rows of a warp
 constexpr int kCols = 256;                   // columns of a step
 
-// Shared-memory plan, as offsets.  The code table comes first; its entries use
-// half of their 256 bytes, and the first tokens' activations sit in the other
-// halves.  After it the other tokens' activations, a line of zeros, staged
-// scales, partial sums, T, the tokens' largest magnitudes and factors.
+// Shared-memory plan, in shared-space addresses.  The code table sits at 64
+// KiB, so that a lane's address in it is its word's byte dropped into bits
+// 8-15 of a constant, with no addition.  Its entries use half of their 256
+// bytes; the first tokens' activations sit in the other halves.  The rest (the
+// other tokens' activations, a line of zeros, staged scales, partial sums, T,
+// the tokens' largest magnitudes and factors) goes before the table, then
+// after it.  Dynamic shared memory begins where the driver's own part (1 KiB)
+// ends; the plan uses none of the first kReserved bytes.
+constexpr uint32_t kReserved = 2048, kLut = 1u << 16;
 struct Plan {
     int unit_rows, span_rows, x_pitch, hole_tokens;
     int raw_pitch, meta_pitch, scale_pitch, red_pitch;    // words (scale_pitch: fp32 of a row in a step)
@@ -112,11 +117,13 @@ inline Plan plan_smem(const PlanKey& k) {
     Plan p;
     p.unit_rows = kRows * (kWarps / k.warps_k);
     p.span_rows = k.span * p.unit_rows;
-    p.total = kLutBytes;
+    int64_t lo = kReserved;
+    p.total = kLut + kLutBytes;
     auto take = [&](int64_t bytes) {
-        const uint32_t at = static_cast<uint32_t>(p.total);
-        p.total += (bytes + 127) / 128 * 128;
-        return at;
+        int64_t& at = lo + bytes <= kLut ? lo : p.total;
+        const uint32_t mine = static_cast<uint32_t>(at);
+        at += (bytes + 127) / 128 * 128;
+        return mine;
     };
     p.x_pitch = ((k.chunks + 1) / 2 * 2) * 256;
     p.hole_tokens = 256 * 128 / p.x_pitch < k.M ? 256 * 128 / p.x_pitch : k.M;
@@ -138,12 +145,21 @@ inline Plan plan_smem(const PlanKey& k) {
     return p;
 }
 
-__device__ __forceinline__ uint4 ldg_weights(const uint8_t* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+// 16 bytes where `in`, else v stays: rows and columns outside give sums that
+// are not stored, or meet zero activations.
+__device__ __forceinline__ void ldg_weights(uint4& v, const uint8_t* p, bool in) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w) : "l"(p), "r"(static_cast<int>(in)));
+}
+// A table entry.  The table is constant once the kernel's first barrier has
+// passed, and the addresses come from words used after it.
+__device__ __forceinline__ uint32_t lds_table(uint32_t addr) {
+    uint32_t v;
+    asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
 }
+
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -180,6 +196,7 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
     constexpr int kPitch = scale_pitch(kGran);
     constexpr int G = !kCol || kGran == 128 ? 1 : kGran == 64 ? 2 : 4;     // columns per token
     extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* const at0 = smem - smem_u32(smem);           // shared-space address to generic
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
     launch_dependents();
@@ -188,9 +205,9 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
     const int M = a.M;
     const int64_t k_beg = int64_t(blockIdx.y) * a.chunks * 128;
     const int kslab = static_cast<int>(min(K - k_beg, int64_t(a.chunks) * 128));
-    float* const scales = reinterpret_cast<float*>(smem + p.scales) + warp * kRows * kPitch;
-    uint32_t* const smax = reinterpret_cast<uint32_t*>(smem + p.misc);
-    float* const sundo = reinterpret_cast<float*>(smem + p.misc + 64);
+    float* const scales = reinterpret_cast<float*>(at0 + p.scales) + warp * kRows * kPitch;
+    uint32_t* const smax = reinterpret_cast<uint32_t*>(at0 + p.misc);
+    float* const sundo = reinterpret_cast<float*>(at0 + p.misc + 64);
 
     // rows of this CTA, and this warp's part of a unit: 32 rows (the wr-th
     // such group of the unit) x steps m0 ... m1 - 1
@@ -210,6 +227,8 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
     // The weight stream runs a step ahead of the products: (lu, lm) is the
     // step it takes next, wp[i] this lane's words of row 8 i + g there.
     uint4 buf[2][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) buf[i >> 2][i & 3] = make_uint4(0u, 0u, 0u, 0u);
     int lu = 0, lm = m0, lrows = 0;
     const uint8_t* wp[4];
     auto seek_weights = [&]() {
@@ -223,9 +242,7 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
         const bool in = lm * kCols + cc * 128 + c * 32 < kslab;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (in && 8 * i < lrows) v = ldg_weights(wp[i] + cc * 64);
-            buf[cc][i] = v;
+            ldg_weights(buf[cc][i], wp[i] + cc * 64, in && 8 * i < lrows);
         }
     };
     auto next_step = [&]() {
@@ -248,7 +265,6 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
     // Stored scales of the span's rows from row n0 on: a warp per row, the
     // words that hold the slice's blocks b0 ... b1, and their groups'
     // constants.
-    const uint32_t base = smem_u32(smem);
     auto copy_scales = [&](int64_t n0) {
         const int64_t all = (a.N * K + (int64_t(1) << a.log2_block) - 1) >> a.log2_block;
         for (int row = warp; row < p.span_rows && n0 + row < r1; row += kWarps) {
@@ -257,14 +273,14 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
             const uint32_t raw = p.raw + row * p.raw_pitch * 4;
             if (kF32) {
                 const float* src = static_cast<const float*>(a.scales) + b0;
-                for (int w = lane; w <= b1 - b0; w += 32) cp_async4(base + raw + w * 4, src + w, 4);
+                for (int w = lane; w <= b1 - b0; w += 32) cp_async4(raw + w * 4, src + w, 4);
             } else {
                 const int64_t w0 = b0 & ~int64_t(3);
                 const uint8_t* src = static_cast<const uint8_t*>(a.scales) + w0;
                 for (int w = lane; w0 + 4 * w <= b1; w += 32)
-                    cp_async4(base + raw + w * 4, src + 4 * w, static_cast<int>(min(all - (w0 + 4 * w), int64_t(4))));
+                    cp_async4(raw + w * 4, src + 4 * w, static_cast<int>(min(all - (w0 + 4 * w), int64_t(4))));
                 const uint32_t meta = p.meta + row * p.meta_pitch * 4;
-                for (int w = lane; w <= (b1 >> 8) - (b0 >> 8); w += 32) cp_async4(base + meta + w * 4, a.meta + (b0 >> 8) + w, 4);
+                for (int w = lane; w <= (b1 >> 8) - (b0 >> 8); w += 32) cp_async4(meta + w * 4, a.meta + (b0 >> 8) + w, 4);
             }
         }
     };
@@ -275,7 +291,7 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
     for (int i = tid; i < 256 * 8; i += kThreads) {
         const int e = i >> 3;
         const uint32_t v = a.code[e & 15] | (uint32_t(a.code[e >> 4]) << 16);
-        *reinterpret_cast<uint4*>(smem + e * 256 + (i & 7) * 16) = make_uint4(v, v, v, v);
+        *reinterpret_cast<uint4*>(at0 + kLut + e * 256 + (i & 7) * 16) = make_uint4(v, v, v, v);
     }
     // activations: each token's largest finite magnitude, then f16 copies
     // scaled by it, zeros past the slice, in the order of the MMAs: 16-byte
@@ -284,9 +300,9 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
     // piece two words of 64 (m2 & 1, exchanged for odd tokens, so that two
     // tokens' loads share no bank).
     if (tid < 16) smax[tid] = 0;
-    if (tid < 8) *reinterpret_cast<uint4*>(smem + p.zero + tid * 16) = make_uint4(0u, 0u, 0u, 0u);
+    if (tid < 8) *reinterpret_cast<uint4*>(at0 + p.zero + tid * 16) = make_uint4(0u, 0u, 0u, 0u);
     auto x_base = [&](int m) {                              // token m's first piece, and the pieces' stride
-        return m < p.hole_tokens ? make_int2(m * (p.x_pitch / 128) * 256 + 128, 256)
+        return m < p.hole_tokens ? make_int2(kLut + m * (p.x_pitch / 128) * 256 + 128, 256)
                                  : make_int2(p.x + (m - p.hole_tokens) * p.x_pitch, 128);
     };
     __syncthreads();
@@ -343,7 +359,7 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
         constexpr bool kWhole = kCol || kGran == 128;       // lane c: columns 32 c ... 32 c + 31
         const int m2 = kWhole ? u & 3 : kGran == 64 ? (u >> 3) * 2 + (u & 1) : u >> 2;
         const int2 xb = x_base(m);
-        uint8_t* at = smem + xb.x + (w >> 4) * 2 * xb.y + (m2 >> 1) * xb.y + ((m2 ^ m) & 1) * 64;
+        uint8_t* at = at0 + xb.x + (w >> 4) * 2 * xb.y + (m2 >> 1) * xb.y + ((m2 ^ m) & 1) * 64;
         // exchanged words: quarter q of a run of 64 or 16 sits in lane
         // 0, 2, 1, 3 for q = 0 ... 3
         if (kWhole || kGran >= 32) {
@@ -379,10 +395,8 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
     uint4 x1[4];
 #pragma unroll
     for (auto& v : x1) v = make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t lane4 = lane * 4;
-    auto code_pair = [&](uint32_t w, uint32_t sel) {
-        return *reinterpret_cast<const uint32_t*>(smem + prmt(w, lane4, sel));
-    };
+    const uint32_t lane_lut = kLut | lane * 4;
+    auto code_pair = [&](uint32_t w, uint32_t sel) { return lds_table(prmt(w, lane_lut, sel)); };
     constexpr int kTok = G == 1 ? 4 : 2;                  // totals per tile: two tokens' or one's, of two rows
     float tot[2][NT][kTok];
 #pragma unroll
@@ -433,7 +447,7 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
         if (NT == 1) {
 #pragma unroll
             for (int m2 = 0; m2 < 4; ++m2)
-                if (xon) x1[m2] = *reinterpret_cast<const uint4*>(smem + ((xa[0] + (m2 >> 1) * xpiece[0]) ^ ((m2 & 1) * 64u)));
+                if (xon) x1[m2] = *reinterpret_cast<const uint4*>(at0 + ((xa[0] + (m2 >> 1) * xpiece[0]) ^ ((m2 & 1) * 64u)));
         }
         float d[NQ][NT][4];
         uint32_t w[NQ][2][4];
@@ -453,7 +467,7 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
             } else if ((j & 1) == 0) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                    x[t] = *reinterpret_cast<const uint4*>(smem + ((xa[t] + (m2 >> 1) * xpiece[t]) ^ ((m2 & 1) * 64u)));
+                    x[t] = *reinterpret_cast<const uint4*>(at0 + ((xa[t] + (m2 >> 1) * xpiece[t]) ^ ((m2 & 1) * 64u)));
             }
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
@@ -512,14 +526,14 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const int i = a.vec_scales ? i0 + e : (lfirst + min(mi * kCols + e * kGran, kslab - kGran)) >> a.log2_block;
-                v[e] = *reinterpret_cast<const float*>(smem + lraw + i * 4);
+                v[e] = *reinterpret_cast<const float*>(at0 + lraw + i * 4);
             }
         } else if (a.vec_scales) {                        // E blocks in a row, in one word each four, in one group
-            const float m = *reinterpret_cast<const float*>(smem + lmeta + ((lb0 + i0) >> 8) * 4);
+            const float m = *reinterpret_cast<const float*>(at0 + lmeta + ((lb0 + i0) >> 8) * 4);
 #pragma unroll
             for (int e = 0; e < E; e += 4) {
-                const uint32_t w = E >= 4 ? *reinterpret_cast<const uint32_t*>(smem + lraw + i0 + e)
-                                          : *reinterpret_cast<const uint16_t*>(smem + lraw + i0);
+                const uint32_t w = E >= 4 ? *reinterpret_cast<const uint32_t*>(at0 + lraw + i0 + e)
+                                          : *reinterpret_cast<const uint16_t*>(at0 + lraw + i0);
                 if (a.scale_fmt == QLORA_SCALES_E4M3) {
 #pragma unroll
                     for (int q = 0; q < (E < 4 ? E : 4); q += 2) {
@@ -543,8 +557,8 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
             for (int e = 0; e < E; ++e) {
                 // columns past the slice repeat its last scale
                 const int i = (lfirst + min(mi * kCols + e * kGran, kslab - kGran)) >> a.log2_block;
-                const uint32_t code = smem[lraw + i];
-                const float m = *reinterpret_cast<const float*>(smem + lmeta + ((lb0 + i) >> 8) * 4);
+                const uint32_t code = at0[lraw + i];
+                const float m = *reinterpret_cast<const float*>(at0 + lmeta + ((lb0 + i) >> 8) * 4);
                 v[e] = __fmul_rn(a.scale_fmt == QLORA_SCALES_U8 ? static_cast<float>(code)
                                  : a.scale_fmt == QLORA_SCALES_E4M3 ? e4m3_to_float(static_cast<uint8_t>(code))
                                                                     : e5m2_to_float(static_cast<uint8_t>(code)), m);
@@ -579,8 +593,8 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
         }
     };
 
-    float* const red = reinterpret_cast<float*>(smem + p.red);
-    float* const sT = reinterpret_cast<float*>(smem + p.t);
+    float* const red = reinterpret_cast<float*>(at0 + p.red);
+    float* const sT = reinterpret_cast<float*>(at0 + p.t);
     for (int u0 = 0; u0 < units; u0 += a.span) {
         const int64_t n0 = r0 + int64_t(u0) * unit_rows;  // the span's first row
         if (u0 > 0) {
@@ -764,9 +778,15 @@ join_slices_kernel(const __grid_constant__ GemvFmtArgs a, int splits) {
 
 template <int kGran, bool kCol, int NT, bool kF32>
 cudaError_t run(const GemvFmtArgs& a, const Plan& p, dim3 grid, cudaStream_t s) {
+    // the plan's addresses hold where dynamic shared memory begins by kReserved
+    int dev = 0, reserved = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev);
+    if (e != cudaSuccess) return e;
+    if (reserved > static_cast<int>(kReserved)) return cudaErrorInvalidConfiguration;
     const int smem = static_cast<int>(p.total);
     auto* kernel = gemv_fmt_kernel<kGran, kCol, NT, kF32>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
