@@ -61,12 +61,12 @@
 // (lookups and products alone, on words already in registers: 81 cycles per
 // 4096 weights, 16.5 us for the 117 MB weight).
 // Measured (us; % of a 6568 GB/s copy on packed words and scales):
-//   28672 x 8192, NF4, blocks of 64, E4M3 scales: 40.0 with 1 token (46%),
-//   45.7 with 4, 71.7 with 8, 95.5 with 16; with rank 16, 1 token, 40.9
-//   28672 x 8192, NF4, blocks of 16, fp32 scales: 66.8 with 1 token, 149 with 16
-//   8192 x 28672, INT4, blocks of 128, fp32 scales: 42.1 with 1 token, 80.9 with 16
-//   11008 x 4096, NF4, blocks of 32, U8 scales, rank 64, 4 tokens: 21.8
-//   4096 x 4096, FP4, blocks of 16, E4M3 scales, 1 token: 8.0; NF4, blocks of 64: 7.4
+//   28672 x 8192, NF4, blocks of 64, E4M3 scales: 37.7 with 1 token (49%),
+//   43.4 with 4, 67.7 with 8, 92 with 16; with rank 16, 1 token, 38.6
+//   28672 x 8192, NF4, blocks of 16, fp32 scales: 64.2 with 1 token, 134 with 16
+//   8192 x 28672, INT4, blocks of 128, fp32 scales: 38.9 with 1 token, 74.9 with 16
+//   11008 x 4096, NF4, blocks of 32, U8 scales, rank 64, 4 tokens: 20.8
+//   4096 x 4096, FP4, blocks of 16, E4M3 scales, 1 token: 7.2; NF4, blocks of 64: 6.6
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -86,15 +86,15 @@ constexpr int kLutBytes = 256 * 256;         // 256 byte values, 64 words apart,
 constexpr int kRows = 32;                    // rows of a warp
 constexpr int kCols = 256;                   // columns of a step
 
-// Shared-memory plan, in shared-space addresses.  The code table sits at 64
-// KiB, so that a lane's address in it is its word's byte dropped into bits
-// 8-15 of a constant, with no addition.  Its entries use half of their 256
-// bytes; the first tokens' activations sit in the other halves.  The rest (the
-// other tokens' activations, a line of zeros, staged scales, partial sums, T,
-// the tokens' largest magnitudes and factors) goes before the table, then
-// after it.  Dynamic shared memory begins where the driver's own part (1 KiB)
-// ends; the plan uses none of the first kReserved bytes.
-constexpr uint32_t kReserved = 2048, kLut = 1u << 16;
+// Shared-memory plan, in shared-space addresses.  The code table comes first,
+// at a constant, so that a lane's address in it is a byte of its word dropped
+// into bits 8-15 of the lane's number times 4, and needs no addition.  Its
+// entries use half of their 256 bytes; the first tokens' activations sit in
+// the other halves.  Then the other tokens' activations, a line of zeros,
+// staged scales, partial sums, T, the tokens' largest magnitudes and factors.
+// Dynamic shared memory begins where the driver's own part (1 KiB) ends; the
+// plan uses none of the first kReserved bytes.
+constexpr uint32_t kReserved = 2048, kLut = kReserved;
 struct Plan {
     int unit_rows, span_rows, x_pitch, hole_tokens;
     int raw_pitch, meta_pitch, scale_pitch, red_pitch;    // words (scale_pitch: fp32 of a row in a step)
@@ -117,13 +117,11 @@ inline Plan plan_smem(const PlanKey& k) {
     Plan p;
     p.unit_rows = kRows * (kWarps / k.warps_k);
     p.span_rows = k.span * p.unit_rows;
-    int64_t lo = kReserved;
     p.total = kLut + kLutBytes;
     auto take = [&](int64_t bytes) {
-        int64_t& at = lo + bytes <= kLut ? lo : p.total;
-        const uint32_t mine = static_cast<uint32_t>(at);
-        at += (bytes + 127) / 128 * 128;
-        return mine;
+        const uint32_t at = static_cast<uint32_t>(p.total);
+        p.total += (bytes + 127) / 128 * 128;
+        return at;
     };
     p.x_pitch = ((k.chunks + 1) / 2 * 2) * 256;
     p.hole_tokens = 256 * 128 / p.x_pitch < k.M ? 256 * 128 / p.x_pitch : k.M;
@@ -152,11 +150,11 @@ __device__ __forceinline__ void ldg_weights(uint4& v, const uint8_t* p, bool in)
                  "@q ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
                  : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w) : "l"(p), "r"(static_cast<int>(in)));
 }
-// A table entry.  The table is constant once the kernel's first barrier has
+// The table entry at an offset.  The table is constant once the kernel's first barrier has
 // passed, and the addresses come from words used after it.
 __device__ __forceinline__ uint32_t lds_table(uint32_t addr) {
     uint32_t v;
-    asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+    asm("ld.shared.b32 %0, [%1 + %2];" : "=r"(v) : "r"(addr), "n"(kLut));
     return v;
 }
 
@@ -395,8 +393,8 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
     uint4 x1[4];
 #pragma unroll
     for (auto& v : x1) v = make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t lane_lut = kLut | lane * 4;
-    auto code_pair = [&](uint32_t w, uint32_t sel) { return lds_table(prmt(w, lane_lut, sel)); };
+    const uint32_t lane4 = lane * 4;
+    auto code_pair = [&](uint32_t w, uint32_t sel) { return lds_table(prmt(w, lane4, sel)); };
     constexpr int kTok = G == 1 ? 4 : 2;                  // totals per tile: two tokens' or one's, of two rows
     float tot[2][NT][kTok];
 #pragma unroll
