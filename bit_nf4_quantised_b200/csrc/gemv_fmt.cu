@@ -62,10 +62,10 @@
 // 4096 weights, 16.5 us for the 117 MB weight).
 // Measured (us; % of a 6568 GB/s copy on packed words and scales):
 //   28672 x 8192, NF4, blocks of 64, E4M3 scales: 37.7 with 1 token (49%),
-//   43.4 with 4, 67.7 with 8, 92 with 16; with rank 16, 1 token, 38.6
-//   28672 x 8192, NF4, blocks of 16, fp32 scales: 64.2 with 1 token, 134 with 16
-//   8192 x 28672, INT4, blocks of 128, fp32 scales: 38.9 with 1 token, 74.9 with 16
-//   11008 x 4096, NF4, blocks of 32, U8 scales, rank 64, 4 tokens: 20.8
+//   43.1 with 4, 67.7 with 8, 90.4 with 16; with rank 16, 1 token, 38.3
+//   28672 x 8192, NF4, blocks of 16, fp32 scales: 64.2 with 1 token, 133 with 16
+//   8192 x 28672, INT4, blocks of 128, fp32 scales: 38.9 with 1 token, 71.9 with 16
+//   11008 x 4096, NF4, blocks of 32, U8 scales, rank 64, 4 tokens: 20.5
 //   4096 x 4096, FP4, blocks of 16, E4M3 scales, 1 token: 7.2; NF4, blocks of 64: 6.6
 #include <cuda_fp16.h>
 
@@ -681,56 +681,58 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
     if (a.part != nullptr) grid_dependency_wait();
 }
 
-// T[m][j] = x[m] . A[j] in fp32: a CTA per rank, its warps on equal runs of
-// the contraction, added in warp order.
+// T[m][j] = x[m] . A[j] in fp32: a CTA per rank and kM tokens (all 16 in one
+// CTA took 12 us at 4096 columns), its warps on equal runs of the contraction,
+// added in warp order.
 constexpr int kTThreads = 512;
 template <int kM>
 __global__ void __launch_bounds__(kTThreads)
 lora_t_kernel(const uint16_t* __restrict__ X, const uint16_t* __restrict__ A, float* __restrict__ T, int M, int64_t K, int r) {
-    __shared__ float part[kTThreads / 32][16];
+    __shared__ float part[kTThreads / 32][kM];
     launch_dependents();
-    const int j = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t n8 = K / 8;
-    const int64_t s0 = n8 * warp / (kTThreads / 32), s1 = n8 * (warp + 1) / (kTThreads / 32);
+    const int j = blockIdx.x, mb = blockIdx.y * kM, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n8 = static_cast<int>(K / 8);
+    const int s0 = n8 * warp / (kTThreads / 32), s1 = n8 * (warp + 1) / (kTThreads / 32);      // K <= 2^24
+    const uint4* const a8 = reinterpret_cast<const uint4*>(A + j * K);
+    const uint4* x8[kM];
     float t[kM];
 #pragma unroll
-    for (int m = 0; m < kM; ++m) t[m] = 0.f;
-#pragma unroll(kM == 1 ? 4 : kM == 4 ? 2 : 1)
-    for (int64_t s = s0 + lane; s < s1; s += 32) {
-        const uint4 av = __ldg(reinterpret_cast<const uint4*>(A + j * K) + s);
+    for (int m = 0; m < kM; ++m) {
+        x8[m] = reinterpret_cast<const uint4*>(X + min(mb + m, M - 1) * K);
+        t[m] = 0.f;
+    }
+#pragma unroll(kM == 1 ? 4 : 2)
+    for (int s = s0 + lane; s < s1; s += 32) {
+        const uint4 av = __ldg(a8 + s);
         const uint32_t aw[4] = {av.x, av.y, av.z, av.w};
 #pragma unroll
         for (int m = 0; m < kM; ++m) {
-            if (m < M) {
-                const uint4 xv = __ldg(reinterpret_cast<const uint4*>(X + m * K) + s);
-                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+            const uint4 xv = __ldg(x8[m] + s);
+            const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    t[m] = fmaf(__uint_as_float(aw[e] << 16), __uint_as_float(xw[e] << 16), t[m]);
-                    t[m] = fmaf(__uint_as_float(aw[e] & 0xffff0000u), __uint_as_float(xw[e] & 0xffff0000u), t[m]);
-                }
+            for (int e = 0; e < 4; ++e) {
+                t[m] = fmaf(__uint_as_float(aw[e] << 16), __uint_as_float(xw[e] << 16), t[m]);
+                t[m] = fmaf(__uint_as_float(aw[e] & 0xffff0000u), __uint_as_float(xw[e] & 0xffff0000u), t[m]);
             }
         }
     }
 #pragma unroll
     for (int m = 0; m < kM; ++m) {
-        if (m < M) {
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) t[m] += __shfl_xor_sync(0xffffffffu, t[m], o);
-            if (lane == 0) part[warp][m] = t[m];
-        }
+        for (int o = 16; o >= 1; o >>= 1) t[m] += __shfl_xor_sync(0xffffffffu, t[m], o);
+        if (lane == 0) part[warp][m] = t[m];
     }
     __syncthreads();
-    if (threadIdx.x < M) {
+    if (threadIdx.x < kM && mb + threadIdx.x < M) {
         float s = 0.f;
         for (int w = 0; w < kTThreads / 32; ++w) s += part[w][threadIdx.x];
-        T[threadIdx.x * r + j] = s;
+        T[(mb + threadIdx.x) * r + j] = s;
     }
 }
 
 // Y[m][n] = bf16(sum of the slices' partial products, in slice order, + gamma
-// T[m] . B[n]): a thread per row n and four tokens.
-constexpr int kJoinTokens = 4;
+// T[m] . B[n]): a thread per row n and two tokens.
+constexpr int kJoinTokens = 2;               // 8192 x 28672, 16 tokens: 71.7 us; with 4 74.7
 __global__ void __launch_bounds__(256)
 join_slices_kernel(const __grid_constant__ GemvFmtArgs a, int splits) {
     grid_dependency_wait();                               // everything comes from the kernels before
@@ -835,7 +837,7 @@ GemvFmtPlan gemv_fmt_plan(int M, int64_t N, int64_t K, int r, int log2_block, bo
     };
     int64_t splits = 1;
     // (many tokens: narrower slices, for the sake of L1: 8192 x 28672 with 16
-    // tokens 86.7 -> 80.9 us)
+    // tokens by 7%)
     while (per_of(splits) > 4 && bytes(splits, kWarps, 1) > (M > 8 ? kSmemSmall : kSmemLimit)) ++splits;
     // few rows: more slices, as long as every warp keeps a step
     const int64_t by_rows = std::max<int64_t>(1, (N + 15) / 16);
@@ -872,8 +874,8 @@ GemvFmtPlan gemv_fmt_plan(int M, int64_t N, int64_t K, int r, int log2_block, bo
 cudaError_t launch_gemv_fmt(GemvFmtArgs a, const GemvFmtPlan& p, cudaStream_t s) {
     const int gran = gran_of(a.log2_block, a.K);
     if (a.t_rank > 0) {
-        auto* kernel = a.M == 1 ? lora_t_kernel<1> : a.M <= 4 ? lora_t_kernel<4> : lora_t_kernel<16>;
-        kernel<<<static_cast<unsigned>(a.t_rank), kTThreads, 0, s>>>(a.X, a.A, a.T, a.M, a.K, a.t_rank);
+        auto* kernel = a.M == 1 ? lora_t_kernel<1> : lora_t_kernel<4>;
+        kernel<<<dim3(static_cast<unsigned>(a.t_rank), static_cast<unsigned>((a.M + 3) / 4)), kTThreads, 0, s>>>(a.X, a.A, a.T, a.M, a.K, a.t_rank);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
