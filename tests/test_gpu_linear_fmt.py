@@ -112,6 +112,15 @@ def test_shapes(q, M, N, K, block, r):
     _check(q, M, N, K, "nf4", block, SCALES[(M + N) % 4], r=r)
 
 
+@pytest.mark.parametrize("M,N,K,block,scales,r", [(1, 200001, 64, 64, "e4m3", 0), (2, 60000, 512, 16, "fp32", 8), (16, 30000, 320, 32, "u8", 0),
+                                                  (16, 2500, 4096, 64, "e5m2", 128), (13, 9001, 1024, 128, "fp32", 64),
+                                                  (9, 700, 16384, 16, "fp32", 16), (8, 148 * 33, 2048, 256, "e4m3", 0)])
+def test_many_rows(q, M, N, K, block, scales, r):
+    """Many rows a CTA: several spans between barriers, ragged last units,
+    slices with an adapter."""
+    _check(q, M, N, K, "nf4", block, scales, r=r)
+
+
 @pytest.mark.parametrize("book", list(BOOKS))
 def test_codebooks(q, book):
     _check(q, 2, 300, 640, book, 64, "fp32")

@@ -115,6 +115,30 @@ def test_backward(q, M, D, res):
     assert x2 is d2 and torch.equal(d2, dX) and torch.equal(acc, 0.5 + dw)
 
 
+@pytest.mark.parametrize("M,D", [(4000, 2056), (1500, 4096), (700, 16384)])
+def test_many_rows_of_a_cta(q, M, D):
+    """More rows than a persistent grid takes at once, past several rounds of
+    its ring: the same bytes as the rows in two halves, which other CTAs take."""
+    h, r, dy, dr, w = _inputs(M, D, M + D)
+    q8 = q.empty_act8(M, D) if D % 64 == 0 else None
+    Y, H = q.qlora_rmsnorm_forward(h, w, 1e-5, residual=r, q8=q8)
+    dX, dw = q.qlora_rmsnorm_backward(dy, H, w, 1e-5, dres=dr)
+    exact = o.rmsnorm(_f(H), _f(w), float(np.float32(1e-5)))
+    _inside(Y, exact, E * np.abs(exact))
+    k = M // 2 + 1
+    for rows in (slice(0, k), slice(k, M)):
+        p8 = q.empty_act8(rows.stop - rows.start, D) if q8 is not None else None
+        Yp, Hp = q.qlora_rmsnorm_forward(h[rows], w, 1e-5, residual=r[rows], q8=p8)
+        dXp, _ = q.qlora_rmsnorm_backward(dy[rows], Hp, w, 1e-5, dres=dr[rows], want_dweight=False)
+        assert torch.equal(Yp, Y[rows]) and torch.equal(Hp, H[rows]) and torch.equal(dXp, dX[rows])
+        if p8 is not None:
+            assert torch.equal(p8.codes, q8.codes.view(M, D)[rows].reshape(-1))
+            assert torch.equal(p8.scales, q8.scales.view(M, D // 64)[rows].reshape(-1))
+    Hf, G = _f(H), _f(dy)
+    term = G * Hf / np.sqrt((Hf * Hf).mean(1, keepdims=True) + float(np.float32(1e-5)))
+    assert (np.abs(_f(dw) - term.sum(0)) <= (E + (M + 8) * 2.0 ** -24) * np.abs(term).sum(0) + 1e-37).all()
+
+
 def test_zero_rows_and_empty_batches(q):
     w = torch.ones(256, device="cuda")
     z = torch.zeros(4, 256, device="cuda").bfloat16()
