@@ -744,14 +744,21 @@ def empty_act8(rows: int, cols: int, code: int = QLORA_ACT8_INT8, device="cuda")
     return Act8(codes, codes.new_empty(rows * cols // ACT8_BLOCK, dtype=torch.float32), rows, cols, code)
 
 
+def _new_act8(rows: int, cols: int, code: int, dev):
+    x8 = empty_act8(rows, cols, code, dev)
+    return x8, _Act8(x8.codes.data_ptr(), x8.scales.data_ptr(), rows, cols, code)
+
+
 def qlora_act8_quantize(X: torch.Tensor, code: int = QLORA_ACT8_INT8, out: Act8 | None = None,
                         stream=None) -> Act8:
     """The 8-bit copy of a bf16 [rows, cols] activation (cols % 64 == 0), in
     `out` with its code if given."""
     M, K, dev = _matrix(X, "X")
     with _on(X, stream):
-        out = out if out is not None else empty_act8(M, K, code, dev)
-        st = out.c_struct(dev, "out", M, K)
+        if out is None:
+            out, st = _new_act8(M, K, code, dev)
+        else:
+            st = out.c_struct(dev, "out", M, K)
         _check(lib().qlora_act8_quantize(X.data_ptr(), st, _raw_stream()), "qlora_act8_quantize")
     return out
 
@@ -760,11 +767,11 @@ def qlora_act8_dequantize(x8: Act8, out: torch.Tensor | None = None, stream=None
     """The bf16 values of an 8-bit copy."""
     dev = x8.codes.device
     with _on(x8.codes, stream):
-        if out is None:
+        po = None if out is None else _arg(out, torch.bfloat16, (x8.rows, x8.cols), dev, "out")
+        if po is None:
             out = torch.empty(x8.rows, x8.cols, dtype=torch.bfloat16, device=dev)
-        _check(lib().qlora_act8_dequantize(x8.c_struct(dev, "x8"),
-                                           _arg(out, torch.bfloat16, (x8.rows, x8.cols), dev, "out"),
-                                           _raw_stream()), "qlora_act8_dequantize")
+            po = out.data_ptr()
+        _check(lib().qlora_act8_dequantize(x8.c_struct(dev, "x8"), po, _raw_stream()), "qlora_act8_dequantize")
     return out
 
 
@@ -775,12 +782,20 @@ def qlora_swiglu_forward_act8(G: torch.Tensor, U: torch.Tensor, code: int = QLOR
     M, F, dev = _matrix(G, "G")
     with _on(G, stream):
         pu = _arg(U, torch.bfloat16, G.shape, dev, "U")
-        H = H if H is not None else torch.empty_like(G)
-        g8 = g8 if g8 is not None else empty_act8(M, F, code, dev)
-        u8 = u8 if u8 is not None else empty_act8(M, F, g8.code, dev)
-        _check(lib().qlora_swiglu_forward_act8(G.data_ptr(), pu, _arg(H, torch.bfloat16, G.shape, dev, "H"),
-                                               g8.c_struct(dev, "g8", M, F), u8.c_struct(dev, "u8", M, F),
-                                               _raw_stream()), "qlora_swiglu_forward_act8")
+        ph = None if H is None else _arg(H, torch.bfloat16, G.shape, dev, "H")
+        if ph is None:
+            H = torch.empty_like(G)
+            ph = H.data_ptr()
+        if g8 is None:
+            g8, sg = _new_act8(M, F, code, dev)
+        else:
+            sg = g8.c_struct(dev, "g8", M, F)
+        if u8 is None:
+            u8, su = _new_act8(M, F, g8.code, dev)
+        else:
+            su = u8.c_struct(dev, "u8", M, F)
+        _check(lib().qlora_swiglu_forward_act8(G.data_ptr(), pu, ph, sg, su, _raw_stream()),
+               "qlora_swiglu_forward_act8")
     return H, g8, u8
 
 
@@ -790,14 +805,18 @@ def qlora_swiglu_backward_act8(dH: torch.Tensor, g8: Act8, u8: Act8, dG: torch.T
     """(dG, dU) from the 8-bit copies; H, if given, receives silu(g~) * u~."""
     M, F, dev = _matrix(dH, "dH")
     with _on(dH, stream):
-        dG = dG if dG is not None else torch.empty_like(dH)
-        dU = dU if dU is not None else torch.empty_like(dH)
+        pg = None if dG is None else _arg(dG, torch.bfloat16, dH.shape, dev, "dG")
+        if pg is None:
+            dG = torch.empty_like(dH)
+            pg = dG.data_ptr()
+        pu = None if dU is None else _arg(dU, torch.bfloat16, dH.shape, dev, "dU")
+        if pu is None:
+            dU = torch.empty_like(dH)
+            pu = dU.data_ptr()
         ph = None if H is None else _arg(H, torch.bfloat16, dH.shape, dev, "H")
         _check(lib().qlora_swiglu_backward_act8(dH.data_ptr(), g8.c_struct(dev, "g8", M, F),
-                                                u8.c_struct(dev, "u8", M, F),
-                                                _arg(dG, torch.bfloat16, dH.shape, dev, "dG"),
-                                                _arg(dU, torch.bfloat16, dH.shape, dev, "dU"), ph,
-                                                _raw_stream()), "qlora_swiglu_backward_act8")
+                                                u8.c_struct(dev, "u8", M, F), pg, pu, ph, _raw_stream()),
+               "qlora_swiglu_backward_act8")
     return dG, dU
 
 
@@ -952,16 +971,22 @@ def qlora_rmsnorm_forward(X: torch.Tensor, weight: torch.Tensor, eps: float,
     with _on(X, stream):
         pw = _arg(weight, torch.float32, (D,), dev, "weight")
         pr = None if residual is None else _arg(residual, bf, X.shape, dev, "residual")
-        if H is None and residual is not None:
+        ph = py = None
+        if H is not None:
+            ph = _arg(H, bf, X.shape, dev, "H")
+        elif residual is not None:
             H = torch.empty_like(X)
+            ph = H.data_ptr()
         if not want_Y:
             Y = None
-        elif Y is None:
+        elif Y is not None:
+            py = _arg(Y, bf, X.shape, dev, "Y")
+        else:
             Y = torch.empty_like(X)
+            py = Y.data_ptr()
         _check(lib().qlora_rmsnorm_forward(
-            X.data_ptr(), pr, pw, M, D, eps, None if H is None else _arg(H, bf, X.shape, dev, "H"),
-            None if Y is None else _arg(Y, bf, X.shape, dev, "Y"),
-            None if q8 is None else q8.c_struct(dev, "q8", M, D), _raw_stream()), "qlora_rmsnorm_forward")
+            X.data_ptr(), pr, pw, M, D, eps, ph, py, None if q8 is None else q8.c_struct(dev, "q8", M, D),
+            _raw_stream()), "qlora_rmsnorm_forward")
     return Y, (X if H is None else H)
 
 
@@ -989,18 +1014,24 @@ def qlora_rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Tens
         ph = _arg(H, bf, dY.shape, dev, "H")
         pw = _arg(weight, f32, (D,), dev, "weight")
         pr = None if dres is None else _arg(dres, bf, dY.shape, dev, "dres")
-        dX = dX if dX is not None else torch.empty_like(dY)
+        px = None if dX is None else _arg(dX, bf, dY.shape, dev, "dX")
+        if px is None:
+            dX = torch.empty_like(dY)
+            px = dX.data_ptr()
+        pdw = None
         if not want_dweight:
             dweight = None
-        elif dweight is None:
+        elif dweight is not None:
+            pdw = _arg(dweight, f32, (D,), dev, "dweight")
+        else:
             if accumulate:
                 raise ValueError("accumulate needs dweight")
-            dweight = dY.new_empty(D, dtype=f32)
+            dweight = torch.empty_like(weight)
+            pdw = dweight.data_ptr()
         if dweight is not None:
             ws = _workspace(ws, _rmsnorm_workspace(M, D, dev.index) if ws is None else 0, dev)
         _check(lib().qlora_rmsnorm_backward(
-            dY.data_ptr(), ph, pr, pw, M, D, eps, _arg(dX, bf, dY.shape, dev, "dX"),
-            None if dweight is None else _arg(dweight, f32, (D,), dev, "dweight"), int(bool(accumulate)),
+            dY.data_ptr(), ph, pr, pw, M, D, eps, px, pdw, int(bool(accumulate)),
             None if dweight is None else ws.data_ptr(), 0 if dweight is None else ws.nbytes, _raw_stream()),
             "qlora_rmsnorm_backward")
     return dX, dweight
@@ -1047,13 +1078,16 @@ def qlora_linear_fmt_forward(X: torch.Tensor, packed: torch.Tensor, scales: torc
             ws = X.new_empty(size, dtype=torch.uint8) if size else None
         else:
             _workspace(ws, 0, dev)
-        Y = Y if Y is not None else X.new_empty(M, N)
+        py = None if Y is None else _arg(Y, bf, (M, N), dev, "Y")
+        if py is None:
+            Y = torch.empty(M, N, dtype=bf, device=dev)
+            py = Y.data_ptr()
         _check(lib().qlora_linear_fmt_forward(
             X.data_ptr(), M, _arg(packed, torch.uint8, (blocks * fmt.block // 2,), dev, "packed"),
             _arg(scales, torch.float32 if f32 else torch.uint8, (blocks,), dev, "scales"),
             None if f32 else _arg(meta, torch.float32, (-(-blocks // GROUP),), dev, "meta"), N, K, st,
             None if A is None else _arg(A, bf, (r, K), dev, "A"),
             None if B is None else _arg(B, bf, (N, r), dev, "B"), r, float(scale),
-            _arg(Y, bf, (M, N), dev, "Y"), None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
+            py, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
             _raw_stream()), "qlora_linear_fmt_forward")
     return Y

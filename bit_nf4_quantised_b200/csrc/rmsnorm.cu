@@ -395,14 +395,18 @@ unsigned grid_for(const Shape& s, int num_sms, int threads_per_sm) {
 int forward_threads(const Shape& s) { return s.nv == 4 && s.block.y == 1 ? 512 : 1024; }
 constexpr int kBackwardThreads = 512;
 
+constexpr int kSmemDefault = 47 * 1024;   // dynamic shared memory beside the static, without asking for more
+
 template <int NV, bool kRes>
 cudaError_t run_forward(const RmsNormArgs& a, const Shape& s, unsigned grid, cudaStream_t st) {
     const int smem = forward_ring(NV, kRes, static_cast<int>(s.block.x * s.block.y));
     auto* kernel = a.q.codes == nullptr ? rmsnorm_forward_kernel<NV, kRes, -1>
                    : a.q.code == QLORA_ACT8_E4M3 ? rmsnorm_forward_kernel<NV, kRes, QLORA_ACT8_E4M3>
                                                  : rmsnorm_forward_kernel<NV, kRes, QLORA_ACT8_INT8>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    if (smem > kSmemDefault) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
     kernel<<<grid, s.block, smem, st>>>(a);
     return cudaGetLastError();
 }
@@ -418,8 +422,10 @@ cudaError_t run_backward(const RmsNormGradArgs& a, const Shape& s, unsigned grid
     const int threads = static_cast<int>(s.block.x * s.block.y);
     const int smem = std::max(backward_ring(NV, kRes, threads), static_cast<int>(s.block.y - 1) * a.D * 4);
     auto* kernel = a.dweight ? rmsnorm_backward_kernel<NV, kRes, true> : rmsnorm_backward_kernel<NV, kRes, false>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    if (smem > kSmemDefault) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
     kernel<<<grid, s.block, smem, st>>>(a);
     return cudaGetLastError();
 }
