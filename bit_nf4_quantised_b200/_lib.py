@@ -720,13 +720,14 @@ class Act8:
         if (rows is not None and r != rows) or (cols is not None and c != cols):
             raise ValueError(f"{name} is {r} x {c}, expected {r if rows is None else rows} x "
                              f"{c if cols is None else cols}")
-        codes, scales = self.codes, self.scales
-        for t, n, what in ((codes, r * c, "codes"), (scales, r * c // ACT8_BLOCK, "scales")):
-            if t.numel() != n or t.device != dev or not t.is_contiguous():
-                raise ValueError(f"{name}.{what} must be a contiguous tensor of {n} values on {dev}")
-        if codes.element_size() != 1 or scales.dtype is not torch.float32 or not codes.is_cuda:
-            raise ValueError(f"{name}: CUDA tensors, codes one byte each, scales torch.float32")
-        return _Act8(codes.data_ptr(), scales.data_ptr(), r, c, self.code)
+        codes, scales, n = self.codes, self.scales, r * c
+        if (codes.numel() == n and scales.numel() == n // ACT8_BLOCK and codes.device == dev and scales.device == dev
+                and codes.is_cuda and codes.is_contiguous() and scales.is_contiguous()
+                and codes.element_size() == 1 and scales.dtype is torch.float32):
+            return _Act8(codes.data_ptr(), scales.data_ptr(), r, c, self.code)
+        raise ValueError(f"{name} must have contiguous codes of {n} one-byte values and {n // ACT8_BLOCK} torch.float32 "
+                         f"scales on {dev}, got {codes.numel()} of {codes.dtype} on {codes.device} and "
+                         f"{scales.numel()} of {scales.dtype} on {scales.device}")
 
 
 def qlora_act8_sizes(rows: int, cols: int):
@@ -1045,16 +1046,21 @@ def qlora_linear_fmt_workspace_size(M: int, N: int, K: int, r: int, fmt: Format)
 
 
 @functools.lru_cache(maxsize=256)
-def _format_struct(codes: tuple, block: int, scales: int) -> _Format:
-    return Format(codes, block, scales).c_struct()
+def _format_entry(codes: tuple, block: int, scales: int):
+    """(the C struct, the workspace sizes asked for so far) of a format."""
+    return Format(codes, block, scales).c_struct(), {}
 
 
-@functools.lru_cache(maxsize=1024)
-def _linear_fmt_workspace(M: int, N: int, K: int, r: int, codes: tuple, block: int, scales: int, device: int) -> int:
-    b = ctypes.c_size_t()                             # of the current device: its number of SMs
-    _check(lib().qlora_linear_fmt_workspace_size(M, N, K, r, _format_struct(codes, block, scales), ctypes.byref(b)),
-           "qlora_linear_fmt_workspace_size")
-    return b.value
+def _linear_fmt_workspace(entry, shape) -> int:
+    st, sizes = entry
+    if shape not in sizes:                            # shape: M, N, K, r, and the device for its number of SMs
+        b = ctypes.c_size_t()
+        _check(lib().qlora_linear_fmt_workspace_size(*shape[:4], st, ctypes.byref(b)),
+               "qlora_linear_fmt_workspace_size")
+        if len(sizes) > 4096:
+            sizes.clear()
+        sizes[shape] = b.value
+    return sizes[shape]
 
 
 def qlora_linear_fmt_forward(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, meta, N: int,
@@ -1068,13 +1074,13 @@ def qlora_linear_fmt_forward(X: torch.Tensor, packed: torch.Tensor, scales: torc
     if (A is None) != (B is None):
         raise ValueError("A and B come together")
     bf = torch.bfloat16
-    blocks = -(-N * K // fmt.block)
+    blocks = -(-N * K // max(fmt.block, 1))           # the library refuses a block below 16
     f32 = fmt.scales == QLORA_SCALES_FP32
     with _on(X, stream):
-        codes = tuple(fmt.codes)
-        st = _format_struct(codes, fmt.block, fmt.scales)
+        entry = _format_entry(tuple(fmt.codes), fmt.block, fmt.scales)
+        st = entry[0]
         if ws is None:
-            size = _linear_fmt_workspace(M, N, K, r, codes, fmt.block, fmt.scales, dev.index)
+            size = _linear_fmt_workspace(entry, (M, N, K, r, dev.index))
             ws = X.new_empty(size, dtype=torch.uint8) if size else None
         else:
             _workspace(ws, 0, dev)

@@ -648,7 +648,8 @@ QLORA_API int qlora_swiglu_backward_act8(const uint16_t* dH, const qlora_act8* g
  * kept in 8 bits: x8 (host struct, M = x8->rows, cols = w->cols) in X's place.
  * X enters only dA = scale (dY B)^T X, and X A^T when T_saved is NULL; both
  * take x~ as it would read back, so every output equals, bit for bit, that
- * of qlora_linear_backward on the dequantised input, which is never written.
+ * of qlora_linear_backward on the dequantised input, which is never written
+ * (gamma U and gamma T enter their products in bf16 there and here).
  * Pass T_saved from the forward to keep dB free of the 8-bit error.
  * Errors: as qlora_linear_backward and qlora_act8_quantize, and
  * QLORA_ERR_SHAPE if x8->cols is not w->cols.

@@ -223,6 +223,19 @@ def test_rows_behind_the_output_and_given_buffers(q):
             bad()
 
 
+def test_formats_that_are_refused(q):
+    N, K = 37, 256
+    dev, _ = _store(N, K, "nf4", 64, "e4m3", 8)
+    good = _fmt(q, "nf4", 64, "e4m3")
+    x = torch.randn(3, K).bfloat16().cuda()
+    for codes, block, scales in ((good.codes, 0, good.scales), (good.codes, 48, good.scales), (good.codes, 8192, good.scales),
+                                 (good.codes[::-1], 64, good.scales), ((0.0, float("nan")), 64, good.scales),
+                                 ((0.0,), 64, good.scales), (good.codes, 64, 7), (good.codes, -64, good.scales)):
+        with pytest.raises(q.QloraError):
+            q.qlora_linear_fmt_forward(x, *dev, N, q.Format(codes, block, scales))
+    assert q.qlora_linear_fmt_forward(x, *dev, N, q.Format(list(good.codes), 64, good.scales)).isfinite().all()
+
+
 def test_same_bytes_streams_and_captured(q):
     """Repeated, concurrent, captured and replayed calls give the same bytes;
     two captured graphs keep their own workspaces."""
