@@ -362,11 +362,13 @@ struct Shape {
     int64_t rows_ctas;   // CTAs if each took blockDim.y rows once
 };
 
-// A warp per row up to kWarpRowMax values.  Above it a CTA per row, with two
-// words a lane (bytes in flight per thread against threads per SM), four
-// where 512 lanes would not cover the row; with fewer rows than SMs one
-// word a lane, for the shortest path through a row.
-Shape shape_for(int64_t M, int D, int num_sms) {
+// A warp per row up to kWarpRowMax values (16384 x 1024, us: forward with the
+// int8 copy 27.4, with a CTA per row 29.9; backward 15.7 and 16.9, with dw 30.9
+// and 28.4).  Above it a CTA per row, with two words a lane, four where 512
+// lanes would not cover the row; in the forward, with fewer rows than SMs, one,
+// for the shortest path through a row (1 x 4096 with the int8 copy: 2.7 us, with
+// two words 3.0; the backward with dw 4.6, with two 4.3).
+Shape shape_for(int64_t M, int D, int num_sms, bool forward) {
     const int nvec = D / 8;
     Shape s;
     if (D <= kWarpRowMax) {
@@ -374,7 +376,7 @@ Shape shape_for(int64_t M, int D, int num_sms) {
         const int64_t per = (M + num_sms - 1) / num_sms;
         s.block = dim3(32, static_cast<unsigned>(per < kWarpRows ? (per < 1 ? 1 : per) : kWarpRows));
     } else {
-        s.nv = nvec > 2 * max_threads(2) ? 4 : M <= num_sms && nvec <= max_threads(1) ? 1 : 2;
+        s.nv = nvec > 2 * max_threads(2) ? 4 : forward && M <= num_sms && nvec <= max_threads(1) ? 1 : 2;
         s.block = dim3(static_cast<unsigned>((nvec + s.nv * 32 - 1) / (s.nv * 32) * 32), 1);
     }
     s.rows_ctas = (M + s.block.y - 1) / s.block.y;
@@ -440,18 +442,18 @@ cudaError_t run_backward(const RmsNormGradArgs& a, const Shape& s, unsigned grid
 int rmsnorm_max_width() { return kMaxWidth; }
 
 int rmsnorm_parts(int64_t M, int D, int num_sms) {
-    return static_cast<int>(grid_for(shape_for(M, D, num_sms), num_sms, kBackwardThreads));
+    return static_cast<int>(grid_for(shape_for(M, D, num_sms, false), num_sms, kBackwardThreads));
 }
 
 cudaError_t launch_rmsnorm_forward(const RmsNormArgs& a, int num_sms, cudaStream_t st) {
-    const Shape s = shape_for(a.M, a.D, num_sms);
+    const Shape s = shape_for(a.M, a.D, num_sms, true);
     const unsigned grid = grid_for(s, num_sms, forward_threads(s));
     return s.nv == 1 ? run_forward<1>(a, s, grid, st)
            : s.nv == 2 ? run_forward<2>(a, s, grid, st) : run_forward<4>(a, s, grid, st);
 }
 
 cudaError_t launch_rmsnorm_backward(const RmsNormGradArgs& a, int num_sms, cudaStream_t st) {
-    const Shape s = shape_for(a.M, a.D, num_sms);
+    const Shape s = shape_for(a.M, a.D, num_sms, false);
     const unsigned grid = grid_for(s, num_sms, kBackwardThreads);
     const cudaError_t e = s.nv == 1 ? run_backward<1>(a, s, grid, st)
                           : s.nv == 2 ? run_backward<2>(a, s, grid, st) : run_backward<4>(a, s, grid, st);
