@@ -62,7 +62,7 @@
 // 4096 weights, 16.5 us for the 117 MB weight).
 // Measured (us; % of a 6568 GB/s copy on packed words and scales):
 //   28672 x 8192, NF4, blocks of 64, E4M3 scales: 37.7 with 1 token (49%),
-//   43.1 with 4, 67.7 with 8, 90.4 with 16; with rank 16, 1 token, 38.3
+//   43.1 with 4, 56.1 with 8, 90.4 with 16; with rank 16, 1 token, 38.3
 //   28672 x 8192, NF4, blocks of 16, fp32 scales: 64.2 with 1 token, 133 with 16
 //   8192 x 28672, INT4, blocks of 128, fp32 scales: 38.9 with 1 token, 71.9 with 16
 //   11008 x 4096, NF4, blocks of 32, U8 scales, rank 64, 4 tokens: 20.5
@@ -809,7 +809,7 @@ cudaError_t run_scales(const GemvFmtArgs& a, const Plan& p, dim3 grid, cudaStrea
 
 // (token, block) columns where one tile of 8 holds them all, exchanged words
 // beyond (us, columns and exchanged: 28672 x 8192, blocks of 64, 1 token 37.2
-// and 41.6, 4 tokens 43.7 and 46.4, 8 tokens in two tiles 80.6 and 67.7; blocks
+// and 41.6, 4 tokens 43.7 and 46.4, 8 tokens in two tiles and one slice 80.6 and 67.7; blocks
 // of 16 with fp32 scales, 2 tokens 67.4 and 76.5; 11008 x 4096, blocks of 32, 4
 // tokens in two tiles 18.4 and 17.1)
 template <int kGran>
@@ -840,9 +840,11 @@ GemvFmtPlan gemv_fmt_plan(int M, int64_t N, int64_t K, int r, int log2_block, bo
                           static_cast<int>(span)}).total;
     };
     int64_t splits = 1;
-    // (many tokens: narrower slices, for the sake of L1: 8192 x 28672 with 16
-    // tokens by 7%)
-    while (per_of(splits) > 4 && bytes(splits, kWarps, 1) > (M > 8 ? kSmemSmall : kSmemLimit)) ++splits;
+    // (several tokens: narrower slices, for the sake of L1; us with slices as
+    // wide as shared memory, and so: 28672 x 8192, blocks of 64, 8 tokens 67.7
+    // and 56.1, blocks of 16, 4 tokens 91.0 and 80.4; 8192 x 28672, 4 tokens 54.7
+    // and 48.5, 16 tokens 79.0 and 71.6; one token has no activations to cut)
+    while (per_of(splits) > 4 && bytes(splits, kWarps, 1) > (M > 1 ? kSmemSmall : kSmemLimit)) ++splits;
     // few rows: more slices, as long as every warp keeps a step
     const int64_t by_rows = std::max<int64_t>(1, (N + 15) / 16);
     while (by_rows * splits * 2 <= num_sms && per_of(splits * 2) >= 2 * kWarps) splits *= 2;
