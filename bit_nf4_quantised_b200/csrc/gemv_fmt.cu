@@ -54,8 +54,8 @@
 //                LoRA term gamma T B^T (T = X A^T from lora_t_kernel, which
 //                runs beside the start of this one).  A barrier for every 32
 //                rows cost 10 us.  Contraction slices, taken where a CTA's
-//                activations would not fit in shared memory, write partial
-//                sums that join_slices_kernel adds.
+//                activations would not fit, or with several tokens would leave
+//                little L1, write partial sums that join_slices_kernel adds.
 // Bound: the shared-memory and L1 pipe: for 4096 weights 64 wavefronts of table
 // loads, and the 2 KiB of packed words pass through it on their way from L2
 // (lookups and products alone, on words already in registers: 81 cycles per
