@@ -784,14 +784,16 @@ cudaError_t run(const GemvFmtArgs& a, const Plan& p, dim3 grid, cudaStream_t s) 
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev);
     if (e != cudaSuccess) return e;
     if (reserved > static_cast<int>(kReserved)) return cudaErrorInvalidConfiguration;
-    const int smem = static_cast<int>(p.total);
+    // The limit belongs to the kernel, not to the call: set to a plan's size,
+    // it would be too low for a larger plan that another host thread is about
+    // to launch.
     auto* kernel = gemv_fmt_kernel<kGran, kCol, NT, kF32>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.total);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -11,11 +11,15 @@ decoding).  The LoRA term: sequential sums of at most K / 8 and r terms in
 fp32.  Then one rounding to bf16."""
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 from oracle import nf4_oracle as o
+
+from _threads import at_once
 
 pytestmark = pytest.mark.gpu
 
@@ -290,3 +294,26 @@ def test_decoding_through_the_block(q):
         assert rel(U, f(y) @ wu.T) < step
         assert rel(H, o.silu(f(G)) * f(U)) < step
         assert rel(out, f(H) @ wd.T) < step
+
+
+@pytest.mark.parametrize("M,block,scales", [(1, 64, "e4m3"), (4, 16, "fp32"), (12, 128, "fp32")])
+def test_host_threads_with_different_sizes(q, M, block, scales):
+    """Calls of one kernel whose plans of shared memory differ, from several
+    host threads at once: none is refused for the other's smaller plan."""
+    f = _fmt(q, "nf4", block, scales)
+    st, calls, outs, refs = f.c_struct(), [], [], []
+    for i, (N, K) in enumerate([(64, 256), (64, 28672), (64, 512), (300, 8192)]):
+        dev, _ = _store(N, K, "nf4", block, scales, i)
+        x = torch.randn(M, K).bfloat16().cuda()
+        refs.append(q.qlora_linear_fmt_forward(x, *dev, N, f))
+        outs.append((torch.empty_like(refs[-1]), x, dev))
+        n = q.qlora_linear_fmt_workspace_size(M, N, K, 0, f)
+        ws = torch.empty(max(n, 256), dtype=torch.uint8, device="cuda")
+        outs[-1] += (ws,)
+        at = [None if t is None else ctypes.c_void_p(t.data_ptr()) for t in (x, *dev, outs[-1][0], ws)]
+        calls.append((q.lib().qlora_linear_fmt_forward,
+                      (at[0], M, *at[1:4], N, K, ctypes.byref(st), None, None, 0, 0.0, at[4], at[5], n, None)))
+    torch.cuda.synchronize()
+    assert at_once(calls, 5000) == [0] * len(calls)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a[0], b) for a, b in zip(outs, refs))
