@@ -399,16 +399,23 @@ constexpr int kBackwardThreads = 512;
 
 constexpr int kSmemDefault = 47 * 1024;   // dynamic shared memory beside the static, without asking for more
 
+// A kernel's limit is a constant, the ring of its largest CTA: set to the size
+// of a call, it would be too low for a larger ring that another host thread is
+// about to launch.
+template <class Kernel>
+cudaError_t allow_smem(Kernel* kernel, int smem, int most) {
+    if (smem <= kSmemDefault) return cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 template <int NV, bool kRes>
 cudaError_t run_forward(const RmsNormArgs& a, const Shape& s, unsigned grid, cudaStream_t st) {
     const int smem = forward_ring(NV, kRes, static_cast<int>(s.block.x * s.block.y));
     auto* kernel = a.q.codes == nullptr ? rmsnorm_forward_kernel<NV, kRes, -1>
                    : a.q.code == QLORA_ACT8_E4M3 ? rmsnorm_forward_kernel<NV, kRes, QLORA_ACT8_E4M3>
                                                  : rmsnorm_forward_kernel<NV, kRes, QLORA_ACT8_INT8>;
-    if (smem > kSmemDefault) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_smem(kernel, smem, forward_ring(NV, kRes, max_threads(NV)));
+    if (e != cudaSuccess) return e;
     kernel<<<grid, s.block, smem, st>>>(a);
     return cudaGetLastError();
 }
@@ -421,13 +428,13 @@ cudaError_t run_forward(const RmsNormArgs& a, const Shape& s, unsigned grid, cud
 template <int NV, bool kRes>
 cudaError_t run_backward(const RmsNormGradArgs& a, const Shape& s, unsigned grid, cudaStream_t st) {
     // the ring; at the end the partial dw of all rows of threads but one
+    constexpr int most = backward_ring(NV, kRes, max_threads(NV));
+    static_assert(most >= (kWarpRows - 1) * kWarpRowMax * 4, "the largest ring holds the partial dw too");
     const int threads = static_cast<int>(s.block.x * s.block.y);
     const int smem = std::max(backward_ring(NV, kRes, threads), static_cast<int>(s.block.y - 1) * a.D * 4);
     auto* kernel = a.dweight ? rmsnorm_backward_kernel<NV, kRes, true> : rmsnorm_backward_kernel<NV, kRes, false>;
-    if (smem > kSmemDefault) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_smem(kernel, smem, most);
+    if (e != cudaSuccess) return e;
     kernel<<<grid, s.block, smem, st>>>(a);
     return cudaGetLastError();
 }

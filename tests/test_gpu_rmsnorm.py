@@ -11,11 +11,15 @@ them, then one rounding to bf16.  In the backward the sum of h t has the same
 depth, relative to the sum of |h t|."""
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 from oracle import nf4_oracle as o
+
+from _threads import at_once
 
 pytestmark = pytest.mark.gpu
 E = 2.0 ** -18
@@ -279,3 +283,27 @@ def test_block_step_on_streams_and_captured(q):
     for outs, _ in kept:
         assert all(torch.equal(a, b) for a, b in zip(outs, new))
     assert not torch.equal(new[1], ref[1])
+
+
+def test_host_threads_with_different_sizes(q):
+    """Calls of one kernel whose rings differ in size, from several host
+    threads at once: none is refused for the other's smaller ring."""
+    fwd, bwd, keep = [], [], []
+    for M, D in ((200, 8192), (200, 6400), (200, 7168), (200, 5120)):
+        x, r, dy, dr, w = _inputs(M, D, D)
+        Y, H = q.qlora_rmsnorm_forward(x, w, 1e-5, residual=r)
+        dX, dw = q.qlora_rmsnorm_backward(dy, x, w, 1e-5, dres=dr)
+        out = [torch.zeros_like(t) for t in (Y, H, dX, dw)]
+        ws = torch.empty(q.qlora_rmsnorm_workspace_size(M, D), dtype=torch.uint8, device="cuda")
+        keep.append((out, (Y, H, dX, dw), x, r, dy, dr, w, ws))
+        p = lambda t: ctypes.c_void_p(t.data_ptr())
+        fwd.append((q.lib().qlora_rmsnorm_forward,
+                    (p(x), p(r), p(w), M, D, 1e-5, p(out[1]), p(out[0]), None, None)))
+        bwd.append((q.lib().qlora_rmsnorm_backward,
+                    (p(dy), p(x), p(dr), p(w), M, D, 1e-5, p(out[2]), p(out[3]), 0, p(ws), ws.numel(), None)))
+    torch.cuda.synchronize()
+    for calls in (fwd, bwd):
+        assert at_once(calls, 5000) == [0] * len(calls)
+    torch.cuda.synchronize()
+    for out, ref, *_ in keep:
+        assert all(torch.equal(a, b) for a, b in zip(out, ref))
