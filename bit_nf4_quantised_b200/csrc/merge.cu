@@ -308,7 +308,10 @@ cudaError_t launch_merge(const MergeArgs* jobs, int n, const Nf4Table& tab, int 
     if (total == 0) return cudaSuccess;
     const int smem = merge_smem_bytes(bt.rp_max);
     const auto kernel = bt.n > 1 ? merge_kernel<true> : merge_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the limit of the largest rank: it belongs to the kernel, and set to this
+    // call's rank it would be too low for another host thread's larger one
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         merge_smem_bytes(QLORA_MAX_RANK));
     if (e != cudaSuccess) return e;
     int per_sm = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);

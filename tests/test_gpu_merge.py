@@ -14,6 +14,8 @@ bits outright.
 """
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -22,6 +24,7 @@ from oracle import nf4_oracle as o
 from bit_nf4_quantised_b200 import synthetic as syn
 
 from _parity import groups_of_rows
+from _threads import at_once
 
 pytestmark = pytest.mark.gpu
 
@@ -205,3 +208,24 @@ def test_requantise_the_oracle_merge(q):
     assert np.array_equal(w2.packed.cpu().numpy(), p2)
     assert np.array_equal(w2.scale_codes.cpu().numpy(), s2)
     assert np.array_equal(w2.meta_scale.cpu().numpy().view(np.uint32), m2.view(np.uint32))
+
+
+def test_host_threads_with_different_ranks(q):
+    """Merges of different ranks, whose shared memory differs, from several
+    host threads at once: none is refused for the other's lower rank."""
+    N, K = 64, 512
+    g = torch.Generator(device="cuda").manual_seed(3)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    w = q.qlora_quantize(0.02 * n(N, K))
+    calls, keep = [], []
+    for r in (8, 128, 16, 64):
+        A, B = (n(r, K) / K ** 0.5).bfloat16(), (0.01 * n(N, r)).bfloat16()
+        ref = q.qlora_merge(w, A, B, 2.0)
+        out = torch.zeros_like(ref)
+        keep.append((out, ref, A, B))
+        p = lambda t: ctypes.c_void_p(t.data_ptr())
+        calls.append((q.lib().qlora_merge, (w.c_struct(), p(A), p(B), r, 2.0, p(out), None)))
+    torch.cuda.synchronize()
+    assert at_once(calls, 5000) == [0] * len(calls)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, ref) for out, ref, *_ in keep)
