@@ -371,7 +371,7 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
             *reinterpret_cast<uint2*>(at) = make_uint2(o.x, o.y);
             *reinterpret_cast<uint2*>(at + 32) = make_uint2(o.z, o.w);
         }
-        if (w == 0) sundo[m] = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) * a.code_undo;
+        if (w == 0) sundo[m] = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
     });
     cp_async_wait<0>();                                     // the scales
     __syncthreads();
@@ -656,7 +656,9 @@ gemv_fmt_kernel(const __grid_constant__ GemvFmtArgs a, const __grid_constant__ P
             const float* src = red + (m * p.span_rows + row) * p.red_pitch;
             float s = 0.f;
             for (int w = 0; w < warps_k; ++w) s += src[w];
-            s *= sundo[m];
+            // in 64 bits: the two factors together, 2^-126 ... 2^113 and 2^-149 ... 2^128,
+            // leave fp32's range where the product need not
+            s = static_cast<float>(s * (sundo[m] * a.code_undo));
             if (a.part != nullptr) {
                 a.part[(int64_t(blockIdx.y) * M + m) * a.N + n] = s;
                 continue;

@@ -255,7 +255,7 @@ struct GemvFmtArgs {
     int M, t_rank;             // t_rank: r, 0 without an adapter
     int log2_block, scale_fmt;
     uint16_t code[16];         // f16 bits of code * factor
-    float code_undo;           // 1 / factor
+    double code_undo;          // 1 / factor
     int chunks;                // 128-wide chunks per contraction slice (the rest by launch_gemv_fmt)
     int64_t rows, extra;       // rows per CTA, and how many CTAs take one more
     int log2_warps;            // log2 of the warps along a slice

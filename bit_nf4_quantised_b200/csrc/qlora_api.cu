@@ -1435,8 +1435,9 @@ namespace {
 // f16 codes of a codebook, times the factor (1, 3, 5, 7 or 15, and the power
 // of two that brings the largest code into [1, 2)) whose rounding errors,
 // relative to each code, are smallest; *undo = 1 / factor.  FP4 (multiples of
-// 1/12) and INT4 (of 1/7) become exact.
-void f16_codes(const qlora_format* f, uint16_t code[16], float* undo) {
+// 1/12) and INT4 (of 1/7) become exact.  (unit is 2^-127 to 2^149: 1 / factor
+// may lie outside fp32's range.)
+void f16_codes(const qlora_format* f, uint16_t code[16], double* undo) {
     double top = 0.0;
     for (int i = 0; i < f->ncodes; ++i) top = std::max(top, std::fabs(double(f->codes[i])));
     const double unit = std::ldexp(1.0, -std::ilogb(top));
@@ -1455,7 +1456,7 @@ void f16_codes(const qlora_format* f, uint16_t code[16], float* undo) {
         if (err < best * 0.999) {
             best = err;
             std::memcpy(code, h, sizeof(h));
-            *undo = static_cast<float>(1.0 / (unit * k));
+            *undo = static_cast<float>(1.0 / k) / unit;
         }
     }
 }

@@ -317,3 +317,28 @@ def test_host_threads_with_different_sizes(q, M, block, scales):
     assert at_once(calls, 5000) == [0] * len(calls)
     torch.cuda.synchronize()
     assert all(torch.equal(a[0], b) for a, b in zip(outs, refs))
+
+
+@pytest.mark.parametrize("size,token", [(68, 80), (68, -80), (68, 100), (-80, -80), (-80, 80), (-80, -20), (-86, 100)])
+def test_codebooks_and_tokens_of_any_size(q, size, token):
+    """Codes of about 2^size, block scales that make weights of about 2^-6 of
+    them, tokens of about 2^token: the factors taken out of codes and
+    activations leave fp32's range together, the products do not.  The bounds
+    are _check's, which no scale changes; the products stay above 2^-126."""
+    N, K = 70, 448
+    codes = (np.array([-3.0, -1.0, -0.4, 0.0, 0.2, 1.0, 5.0], np.float64) * 2.0 ** size).astype(np.float32)
+    g = np.random.default_rng(abs(size) + abs(token))
+    idx = g.integers(0, len(codes), N * K).astype(np.uint8)
+    idx[2 * K: 3 * K] = 3                                     # a row of zeros
+    c = np.exp2(g.uniform(-8, -4, N * K // 64) - size).astype(np.float32)
+    w = (codes.astype(np.float64)[idx].reshape(-1, 64) * c.astype(np.float64)[:, None]).reshape(N, K)
+    x = torch.from_numpy(g.standard_normal((3, K)) * 2.0 ** token).bfloat16()
+    x[1] = 0.0
+    packed = torch.from_numpy(idx[::2] | idx[1::2] << 4).cuda()
+    f = q.Format(tuple(float(v) for v in codes), 64, q.QLORA_SCALES_FP32)
+    Y = q.qlora_linear_fmt_forward(x.cuda(), packed, torch.from_numpy(c).cuda(), None, N, f).double().cpu().numpy()
+    X = x.double().numpy()
+    exact, err = X @ w.T, (2.0 ** -11 + 2.0 ** -16) * (np.abs(X) @ np.abs(w).T)
+    lo, hi = _values(o.bf16_rne_f64(exact - err)), _values(o.bf16_rne_f64(exact + err))
+    assert ((Y >= lo) & (Y <= hi)).all()
+    assert not Y[1].any() and not Y[:, 2].any()
