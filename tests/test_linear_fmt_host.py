@@ -3,6 +3,8 @@ refusals (fake pointers that no kernel ever sees)."""
 from __future__ import annotations
 
 import ctypes
+import pathlib
+import re
 
 import pytest
 import torch
@@ -74,3 +76,21 @@ def test_python_refuses_before_the_library(q):
     p, s, m = torch.zeros(64 * 32, dtype=torch.uint8), torch.zeros(64, dtype=torch.uint8), torch.zeros(1)
     with pytest.raises(ValueError):
         q.qlora_linear_fmt_forward(x, p, s, m, 64, _fmt(q))
+
+
+def test_table_lookups_stay_behind_their_barrier():
+    """An asm that reads memory without being volatile may be moved by the
+    compiler to wherever its operands exist.  The code table's lookup is the
+    only one here; its address is made of packed words, and those that are
+    loaded before the table is complete pass through a volatile asm that
+    clobbers memory, behind the barrier that completes it."""
+    src = (pathlib.Path(__file__).parents[1] / "bit_nf4_quantised_b200" / "csrc" / "gemv_fmt.cu").read_text()
+    free = [a for a in re.findall(r"\basm\s*\(.*?\);", src, re.S) if re.search(r"\bld\.", a)]
+    assert len(free) == 1 and "kLut" in free[0]
+    assert re.search(r"void ldg_weights\([^{]*\{\s*asm volatile\(", src)        # later words: volatile, so after it
+    tie = re.search(r"void after_barrier\(uint4& v\) \{\s*asm volatile\((.*?)\);", src, re.S)
+    assert tie and all(f'"+r"(v.{c})' in tie.group(1) for c in "xyzw") and '"memory"' in tie.group(1)
+    filled = src.index("// code table: byte e of lane l")
+    barrier = src.index("__syncthreads();", src.index("cp_async_wait<0>();", filled))
+    tied = src.index("for (int i = 0; i < 8; ++i) after_barrier(buf[i >> 2][i & 3]);")
+    assert filled < barrier < tied < src.index("auto code_pair") and "uint4 buf[2][4];" in src
