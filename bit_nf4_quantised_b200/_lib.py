@@ -826,10 +826,13 @@ _quantized_sizes = functools.lru_cache(maxsize=1024)(qlora_quantized_sizes)
 
 def _nf4_struct(w: NF4Tensor, dev, name: str) -> _Tensor:
     p, c, m = _quantized_sizes(w.rows, w.cols)
-    for t, n, what in ((w.packed, p, "packed"), (w.scale_codes, c, "scale_codes"),
-                       (w.meta_scale, m // 4, "meta_scale")):
-        if t.numel() < n or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name}.{what} must be a contiguous tensor of {n} values on {dev}")
+    for t, n, what, typed in ((w.packed, p, "packed", w.packed.element_size() == 1),
+                              (w.scale_codes, c, "scale_codes", w.scale_codes.element_size() == 1),
+                              (w.meta_scale, m // 4, "meta_scale", w.meta_scale.dtype is torch.float32)):
+        if t.numel() < n or t.device != dev or not t.is_contiguous() or not typed:
+            raise ValueError(f"{name}.{what} must be a contiguous tensor of {n} "
+                             f"{'torch.float32' if what == 'meta_scale' else 'one-byte'} values on {dev}, got "
+                             f"{t.numel()} of {t.dtype} on {t.device}")
     return w.c_struct()
 
 

@@ -224,3 +224,22 @@ def test_python_refuses_before_the_library(q):
         q.empty_act8(4, 100, device="cpu")
     x8 = q.empty_act8(4, 128, q.QLORA_ACT8_E4M3, device="cpu")
     assert x8.codes.dtype == torch.float8_e4m3fn and x8.nbytes == 512 + 32
+
+
+def test_nf4_weights_of_another_type_are_refused(q):
+    """The calls above count an NF4 weight's values; a half-width constant
+    would be read past its end."""
+    dev, n = torch.device("cpu"), q.qlora_quantized_sizes(64, 256)
+    good = lambda: q.NF4Tensor(torch.zeros(n[0], dtype=torch.uint8), torch.zeros(n[1], dtype=torch.uint8),
+                               torch.zeros(n[2] // 4), 64, 256)
+    q._lib._nf4_struct(good(), dev, "w")
+    w = good()
+    w.scale_codes = w.scale_codes.view(torch.float8_e4m3fn)        # the codes under their own type
+    q._lib._nf4_struct(w, dev, "w")
+    for name, t in (("packed", torch.int16), ("packed", torch.float32), ("scale_codes", torch.bfloat16),
+                    ("meta_scale", torch.float16), ("meta_scale", torch.bfloat16), ("meta_scale", torch.float64),
+                    ("meta_scale", torch.int32)):
+        w = good()
+        setattr(w, name, getattr(w, name).to(t))
+        with pytest.raises(ValueError, match=f"w.{name}"):
+            q._lib._nf4_struct(w, dev, "w")
