@@ -1471,6 +1471,16 @@ int check_linear_fmt(int64_t M, int64_t N, int64_t K, int r, const qlora_format*
     return QLORA_OK;
 }
 
+// A buffer of a call; one of no bytes overlaps nothing.
+struct Span {
+    const void* p;
+    int64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+    const auto x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.bytes > 0 && b.bytes > 0 && x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
+}
+
 // Workspace: T, and the partial products where a second kernel joins them.
 int64_t linear_fmt_bytes(const GemvFmtPlan& p, int64_t M, int64_t N, int r, int64_t* off_t, int64_t* off_part) {
     *off_t = 0;
@@ -1516,6 +1526,15 @@ int qlora_linear_fmt_forward(const uint16_t* X, int64_t M, const uint8_t* packed
         if (!ws || ws_bytes < static_cast<size_t>(need)) return QLORA_ERR_WORKSPACE;
         if (!aligned(ws, kAlign)) return QLORA_ERR_ALIGN;
     }
+    // Y and ws against the inputs and each other
+    const int64_t blocks = cdiv(N * K, fa.block);
+    const bool f32 = fa.scale_fmt == QLORA_SCALES_FP32;
+    const Span in[] = {{X, M * K * 2}, {packed, blocks * fa.block / 2}, {scales, blocks * (f32 ? 4 : 1)},
+                       {meta, f32 ? 0 : cdiv(blocks, QLORA_GROUP) * 4}, {A, r * K * 2}, {B, N * r * 2}};
+    const Span y{Y, M * N * 2}, w{ws, need};
+    for (const Span& i : in)
+        if (overlap(y, i) || overlap(w, i)) return QLORA_ERR_UNSUPPORTED;
+    if (overlap(y, w)) return QLORA_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     GemvFmtArgs a{};
     a.packed = packed;

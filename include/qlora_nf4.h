@@ -252,10 +252,11 @@ QLORA_API int qlora_dequantize_fmt(const uint8_t* packed, const void* scales, co
  *   Y       (device, bf16, M x N, written)
  *   ws      (device, >= qlora_linear_fmt_workspace_size bytes, 256-byte
  *           aligned; may be NULL when that is 0)
+ * Y and ws overlap neither an input nor each other.
  * Shape rules: K % 64 == 0, 64 <= K <= 2^24, 1 <= N < 2^31.  More tokens: expand the weight
  * with qlora_dequantize_fmt and use a matrix product.
  * Errors: QLORA_ERR_NULL, QLORA_ERR_SHAPE, QLORA_ERR_UNSUPPORTED (the format,
- * M, N, K or r), QLORA_ERR_ALIGN (X, Y, A, B, packed and fp32 scales 16-byte;
+ * M, N, K or r; buffers that overlap), QLORA_ERR_ALIGN (X, Y, A, B, packed and fp32 scales 16-byte;
  * 8-bit scales and meta 4-byte), QLORA_ERR_WORKSPACE, QLORA_ERR_CUDA.
  */
 QLORA_API int qlora_linear_fmt_workspace_size(int64_t M, int64_t N, int64_t K, int r,

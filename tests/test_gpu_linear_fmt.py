@@ -342,3 +342,21 @@ def test_codebooks_and_tokens_of_any_size(q, size, token):
     lo, hi = _values(o.bf16_rne_f64(exact - err)), _values(o.bf16_rne_f64(exact + err))
     assert ((Y >= lo) & (Y <= hi)).all()
     assert not Y[1].any() and not Y[:, 2].any()
+
+
+def test_buffers_one_behind_the_other(q):
+    """Buffers that touch but do not overlap are taken; a Y on X is refused."""
+    M, N, K, r = 2, 64, 256, 8
+    dev, _ = _store(N, K, "nf4", 64, "e4m3", 8)
+    f = _fmt(q, "nf4", 64, "e4m3")
+    x, A, B = (torch.randn(*s).bfloat16().cuda() for s in ((M, K), (r, K), (N, r)))
+    ref = q.qlora_linear_fmt_forward(x, *dev, N, f, A=A, B=B, scale=2.0)
+    one = torch.empty(M * K + M * N + r * K + N * r, dtype=torch.bfloat16, device="cuda")
+    X1, Y1, A1, B1 = (t.view(s) for t, s in zip(one.split([M * K, M * N, r * K, N * r]), ((M, K), (M, N), (r, K), (N, r))))
+    for a, b in ((X1, x), (A1, A), (B1, B)):
+        a.copy_(b)
+    assert torch.equal(q.qlora_linear_fmt_forward(X1, *dev, N, f, A=A1, B=B1, scale=2.0, Y=Y1), ref)
+    assert torch.equal(X1, x) and torch.equal(A1, A) and torch.equal(B1, B)
+    with pytest.raises(q.QloraError):
+        q.qlora_linear_fmt_forward(X1, *dev, N, f, A=A1, B=B1, scale=2.0, Y=one[: M * N].view(M, N))
+    assert torch.equal(X1, x)

@@ -94,3 +94,32 @@ def test_table_lookups_stay_behind_their_barrier():
     barrier = src.index("__syncthreads();", src.index("cp_async_wait<0>();", filled))
     tied = src.index("for (int i = 0; i < 8; ++i) after_barrier(buf[i >> 2][i & 3]);")
     assert filled < barrier < tied < src.index("auto code_pair") and "uint4 buf[2][4];" in src
+
+
+@pytest.mark.parametrize("scales", ["E4M3", "FP32"])
+def test_outputs_that_overlap_are_refused(q, scales):
+    """Y and the workspace may lie on no input and not on each other: every
+    CTA reads all of X, A and the constants while others already store."""
+    L, E = q.lib(), q._lib
+    f = _fmt(q, 16, getattr(q, f"QLORA_SCALES_{scales}"))
+    M, N, K, r = 3, 40, 128, 8
+    packed, sc, meta = q.qlora_format_sizes(N * K, f)
+    need = q.qlora_linear_fmt_workspace_size(M, N, K, r, f)
+    sizes = {"X": 2 * M * K, "packed": packed, "scales": sc, "meta": meta, "A": 2 * r * K, "B": 2 * N * r, "Y": 2 * M * N, "ws": need}
+    at = {k: FAKE + 0x10000 * i for i, k in enumerate(sizes)}
+    if not meta:
+        sizes.pop("meta")
+        at["meta"] = None
+
+    def call(p):
+        return L.qlora_linear_fmt_forward(p["X"], M, p["packed"], p["scales"], p["meta"], N, K, f.c_struct(), p["A"], p["B"], r, 2.0,
+                                          p["Y"], p["ws"], need, None)
+    for out in ("Y", "ws"):
+        step = 16 if out == "Y" else 256
+        for other in sizes:
+            if other == out:
+                continue
+            first = at[other] - (sizes[out] - 1) // step * step                # the last place that still touches it
+            last = at[other] + (sizes[other] - 1) // step * step
+            for place in (at[other], first, last):
+                assert call({**at, out: place}) == E.QLORA_ERR_UNSUPPORTED, (out, other, place - at[other])
