@@ -16,7 +16,10 @@
 //                bf16 rounding of Y allows 2^-8.
 //   activations  times a power of two per token that puts the token's largest
 //                value in [2^14, 2^15): their 8 bits are exact in f16 down to
-//                2^-28 of the largest; below, off by 2^-40 of it.
+//                2^-28 of the largest; below, off by half a step of the f16
+//                subnormals, 2^-25 or 2^-39 of the largest.  The power is 2^126
+//                at most; where that is too little, for tokens below 2^-112,
+//                every value is exact, a multiple of 2^-133 2^126.
 // Both factors are taken out of the sums at the end.
 //
 // A CTA per SM, 16 warps, each on 32 rows and a share of the contraction, in

@@ -242,8 +242,9 @@ QLORA_API int qlora_dequantize_fmt(const uint8_t* packed, const void* scales, co
  * One pass over the packed weight; W is not rounded to bf16 on the way.  Each
  * code enters rounded to f16 after a common factor (FP4 and INT4 codes
  * exactly, others within 2^-11 of themselves, or 2^-25 of the largest), the
- * activations exactly down to 2^-28 of their token's largest value and the
- * scales in fp32; sums are fp32, Y is rounded once.  Block scales above 2^90
+ * activations exactly down to 2^-28 of their token's largest value (below,
+ * within 2^-39 of that value) and the scales in fp32; sums are fp32, Y is
+ * rounded once.  Block scales above 2^90
  * may overflow the sums on the way.
  *   X       (device, bf16, M x K, read), 0 <= M <= 16 (M = 0 launches nothing)
  *   packed, scales, meta (device, read): as qlora_quantize_fmt writes them

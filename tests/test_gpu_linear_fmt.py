@@ -344,6 +344,34 @@ def test_codebooks_and_tokens_of_any_size(q, size, token):
     assert not Y[1].any() and not Y[:, 2].any()
 
 
+def test_activations_far_below_their_tokens_largest(q):
+    """A value is exact down to 2^-28 of its token's largest; below that its
+    f16 copy is off by half a step of the subnormals, 2^-25, where the largest
+    is at least 2^14: 2^-39 of the largest.  A token below 2^-112 meets its
+    factor's limit, 2^126, and is exact: bf16 values are multiples of 2^-133,
+    so there of 2^-7, with 8 bits.  The largest value meets a weight of zero,
+    so that it does not hide the others.  Outputs below 2^-126 are rounded to
+    fp32's last step, 2^-149, on the way."""
+    K, N = 64, 40
+    dev, w = _store(N, K, "int4", 64, "fp32", 12)
+    idx = o.unpack_nibbles(dev[0].cpu().numpy(), N * K).reshape(N, K).copy()
+    idx[:, 0] = list(BOOKS["int4"]).index(0.0)
+    w = w.copy()
+    w[:, 0] = 0.0
+    packed = torch.from_numpy(idx.reshape(-1)[::2] | idx.reshape(-1)[1::2] << 4).cuda()
+    steps = 1 + torch.arange(K) / 128
+    x = torch.stack([steps * 2.0 ** -28, steps * 2.0 ** -33,
+                     torch.arange(1, K + 1) * 2.0 ** -120 / 100,                     # 2^-120.6 and below
+                     torch.arange(K, 0, -1) * 2.0 ** -133]).bfloat16()               # subnormals
+    x[:2, 0] = 1.0
+    Y = q.qlora_linear_fmt_forward(x.cuda(), packed, dev[1], None, N, _fmt(q, "int4", 64, "fp32")).double().cpu().numpy()
+    X = x.double().numpy()
+    exact, err = X @ w.T, 2.0 ** -16 * (np.abs(X) @ np.abs(w).T) + 2.0 ** -149
+    err[1] += 2.0 ** -39 * np.abs(w).sum(1)
+    lo, hi = _values(o.bf16_rne_f64(exact - err)), _values(o.bf16_rne_f64(exact + err))
+    assert ((Y >= lo) & (Y <= hi)).all()
+
+
 def test_buffers_one_behind_the_other(q):
     """Buffers that touch but do not overlap are taken; a Y on X is refused."""
     M, N, K, r = 2, 64, 256, 8
