@@ -59,15 +59,27 @@
 //                rows cost 10 us.  Contraction slices, taken where a CTA's
 //                activations would not fit, or with several tokens would leave
 //                little L1, write partial sums that join_slices_kernel adds.
-// Bound: the shared-memory and L1 pipe: for 4096 weights 64 wavefronts of table
-// loads, and the 2 KiB of packed words pass through it on their way from L2
-// (lookups and products alone, on words already in registers: 81 cycles per
-// 4096 weights, 16.5 us for the 117 MB weight).
+// Bound: no unit, but the 16 warps' latencies.
+//   1 token (28672 x 8192): about the sum of reading the packed words alone,
+//   21.0 us, and of lookups and products alone on words already in registers,
+//   16.5 us (81 cycles per 4096 weights).  The two overlap little: a warp asks
+//   for a chunk's successor when it has used the chunk up, and 194 rows a CTA
+//   are 6 groups of 32 and one of 2 for the 8 groups of warps.  The busiest
+//   unit is the shared-memory and L1 pipe, at 66% of its peak (for 4096 weights
+//   64 wavefronts of table loads, and the 2 KiB of packed words from L2 pass
+//   through it too); DRAM 38%.
+//   16 tokens (8192 x 28672): that pipe 49%, issue slots 47%, DRAM 22%, tensor
+//   cores 21%.  The warps wait for fixed-latency results and shared loads,
+//   four of them a scheduler; a CTA's 683 rows are units of 256 in spans with
+//   a barrier between, and each slice's 12 CTAs convert the same activations.
+// Registers: instances with exchanged words spill, one tile 4 bytes a thread
+// (blocks of 16) to 24 (32), two tiles 16 (16), 44 (32; 64 with fp32 scales) and
+// 92 (64 with 8-bit scales); the others do not.
 // Measured (us; % of a 6568 GB/s copy on packed words and scales):
-//   28672 x 8192, NF4, blocks of 64, E4M3 scales: 37.7 with 1 token (49%),
-//   43.1 with 4, 56.1 with 8, 90.4 with 16; with rank 16, 1 token, 38.3
-//   28672 x 8192, NF4, blocks of 16, fp32 scales: 64.2 with 1 token, 133 with 16
-//   8192 x 28672, INT4, blocks of 128, fp32 scales: 38.9 with 1 token, 71.9 with 16
+//   28672 x 8192, NF4, blocks of 64, E4M3 scales: 37.3 with 1 token (50%),
+//   43.2 with 4, 56.2 with 8, 90.8 with 16; with rank 16, 1 token, 38.4
+//   28672 x 8192, NF4, blocks of 16, fp32 scales: 64.3 with 1 token, 134 with 16
+//   8192 x 28672, INT4, blocks of 128, fp32 scales: 38.8 with 1 token, 72.3 with 16
 //   11008 x 4096, NF4, blocks of 32, U8 scales, rank 64, 4 tokens: 20.5
 //   4096 x 4096, FP4, blocks of 16, E4M3 scales, 1 token: 7.2; NF4, blocks of 64: 6.6
 #include <cuda_fp16.h>

@@ -164,9 +164,9 @@ int gemm_col_granule(bool trans);
 //   p_kmajor: P stored [I][C] (ld = ldp) else [C][I].
 //   q_kmajor: Q stored [J][C] (ld = ldq) else [C][J].
 //   err_zero: if set, one thread stores 0 there (clears the call's error word).
-constexpr int kMaxSkinnySplits = 8;
 //   P8, Pscale, p_code: P in blockwise 8 bits instead (P8 != null, P unused;
 //             q_kmajor == p_kmajor; ldp a multiple of 64 and, K-major, so is C)
+constexpr int kMaxSkinnySplits = 8;
 struct SkinnyArgs {
     const uint16_t* P;
     const uint16_t* Q;
@@ -224,7 +224,7 @@ cudaError_t launch_gemv(const CUtensorMap& tm_packed, const GemvArgs& a, int num
                         cudaStream_t stream);
 
 // T = sum of the t_parts partials (also to T_save);
-// Y = bf16(sum_s part[s] + gamma T B^T), without T and B when r = 0
+// Y = bf16(sum_s part[s] + gamma T B^T)
 struct GemvFinalizeArgs {
     const float* part;
     const float* Tpart;

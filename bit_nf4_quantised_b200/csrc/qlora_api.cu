@@ -1514,7 +1514,7 @@ int qlora_linear_fmt_forward(const uint16_t* X, int64_t M, const uint8_t* packed
     if (M == 0) return QLORA_OK;
     if (!X || !Y || !packed || !scales || (fa.scale_fmt != QLORA_SCALES_FP32 && !meta)) return QLORA_ERR_NULL;
     if (r > 0 && (!A || !B)) return QLORA_ERR_NULL;
-    // fp32 scales are read 16 bytes at a time
+    // fp32 scales: 16 bytes, as any fp32 buffer of the interface
     if (!aligned(X, 16) || !aligned(Y, 16) || !aligned(packed, 16) || !aligned(meta, 4) ||
         !aligned(scales, fa.scale_fmt == QLORA_SCALES_FP32 ? 16 : 4) ||
         (r > 0 && (!aligned(A, 16) || !aligned(B, 16))))

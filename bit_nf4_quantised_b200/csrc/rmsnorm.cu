@@ -20,8 +20,13 @@
 // Measured, us, % of a 6568 GB/s copy: 8192 x 4096 forward with residual 47.3
 // (86%), with the int8 copy 55.2 (84%); backward with residual and dw 46.4
 // (88%), without either 34.7 (88%); 513 x 1088 forward 2.6, backward 6.5;
-// 1 x 4096 forward 2.5.  1024 x 16384: forward 20.6 (99%), backward with
-// residual and dw 31.1 (66%: dw and its partial rows are as much as 160 rows).
+// 1 x 4096 forward 2.6.  At both ends of the widths dw costs more than its
+// traffic, for a cause not found: with residual and dw 1024 x 16384 30.8 (66%; the
+// partial rows of dw, written and read, are as much as 160 rows, 3 us of the 10
+// above the copy's time) and 16384 x 1024 30.6 (67%; 1.2 MB of them, nothing),
+// without dw and residual 17.2 (89%) and 15.1.  Forward 1024 x 16384 20.5.
+// Spills, bytes a thread: forward with an 8-bit copy and two words a lane 12
+// (with residual 20), backward with residual, dw and one word 12.
 #include <algorithm>
 
 #include "act8.cuh"
@@ -363,8 +368,8 @@ struct Shape {
 };
 
 // A warp per row up to kWarpRowMax values (16384 x 1024, us: forward with the
-// int8 copy 27.4, with a CTA per row 29.9; backward 15.7 and 16.9, with dw 30.9
-// and 28.4).  Above it a CTA per row, with two words a lane, four where 512
+// int8 copy 27.4, with a CTA per row 29.9; backward 15.7 and 16.9, but with dw 30.9
+// and 28.4: the rule is the forward's and the frozen norm's, and costs dw 2.5).  Above it a CTA per row, with two words a lane, four where 512
 // lanes would not cover the row; in the forward, with fewer rows than SMs, one,
 // for the shortest path through a row (1 x 4096 with the int8 copy: 2.7 us, with
 // two words 3.0; the backward with dw 4.6, with two 4.3).

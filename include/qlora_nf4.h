@@ -16,6 +16,9 @@
  *   - bf16 tensors are passed as uint16_t* holding IEEE bfloat16 bit patterns
  *     (the layout of __nv_bfloat16 and torch.bfloat16).
  *   - All matrices are row-major and densely packed (row stride = columns).
+ *   - Outputs and workspaces overlap neither inputs nor one another, unless
+ *     the entry point says which output may be which input (then exactly that
+ *     buffer).  Only where its errors say so is this checked.
  *   - `stream` is a cudaStream_t (NULL = legacy default stream).  All device
  *     work is enqueued asynchronously on it; a call returns once its kernels
  *     are launched.  Outputs are valid after the stream reaches that point.
@@ -254,6 +257,9 @@ QLORA_API int qlora_dequantize_fmt(const uint8_t* packed, const void* scales, co
  *   ws      (device, >= qlora_linear_fmt_workspace_size bytes, 256-byte
  *           aligned; may be NULL when that is 0)
  * Y and ws overlap neither an input nor each other.
+ * An NF4 weight in blocks of 64 with E4M3 scales can be multiplied by
+ * qlora_linear_forward too: that one takes W~ rounded to bf16, as training
+ * does; this one is faster.
  * Shape rules: K % 64 == 0, 64 <= K <= 2^24, 1 <= N < 2^31.  More tokens: expand the weight
  * with qlora_dequantize_fmt and use a matrix product.
  * Errors: QLORA_ERR_NULL, QLORA_ERR_SHAPE, QLORA_ERR_UNSUPPORTED (the format,
